@@ -11,6 +11,7 @@
 
 #include "../../include/qgemm.h"
 #include "common.cuh"
+#include "i8.cuh"
 
 namespace qg {
 cudaError_t launch_prep(const PrepParams& pp, cudaStream_t stream);
@@ -32,6 +33,21 @@ cudaError_t launch_pack(int fmt, const float* W, int64_t N, int64_t K, void* cod
                         float* tensor_scale, cudaStream_t stream);
 cudaError_t launch_repack(const RepackParams& rp, cudaStream_t stream);
 cudaError_t launch_reduce(const ReduceParams& rp, cudaStream_t stream);
+size_t moe_sort_bytes(int64_t S, int E);
+cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, int* hist,
+                            cudaStream_t stream);
+cudaError_t launch_moe_gather(const void* x, int64_t T, int64_t row_bytes, int k, const int* row,
+                              void* xs, cudaStream_t stream);
+cudaError_t launch_moe_combine(bool in_bf16, bool out_bf16, const void* ys, int64_t T, int64_t H,
+                               int k, const int* row, const float* w, void* y, cudaStream_t stream);
+cudaError_t launch_moe_combine_grad(bool dy_bf16, bool ys_bf16, const void* dy, const void* ys,
+                                    int64_t T, int64_t H, int k, const int* row, const float* w,
+                                    void* dys, float* dw, cudaStream_t stream);
+cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                           cudaStream_t stream);
+cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales,
+                            cudaStream_t stream);
+cudaError_t launch_i8_gemm(const I8Params& p, cudaStream_t stream);
 int* device_error_word();
 }  // namespace qg
 
@@ -1067,6 +1083,269 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x, int64_t M, int64_t K, const voi
     if (e != cudaSuccess) return cuda_fail(e, "SiLU pass launch");
   }
   return QGEMM_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Routed tokens: sorted by expert, and back
+// ---------------------------------------------------------------------------------------
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool row_dtype(int d) { return d == QGEMM_Y_F32 || d == QGEMM_Y_BF16; }
+// T tokens of k slots, rows of H elements
+int check_routed(int64_t T, int k, int64_t H) {
+  if (T < 1 || k < 1 || H < 1 || H > 0x7FFFFFFF || T > 0x7FFFFFFF / k) return QGEMM_ERR_SHAPE;
+  return QGEMM_OK;
+}
+}  // namespace
+
+int qgemm_moe_dispatch_workspace_size(int64_t T, int k, int E, size_t* bytes) {
+  const int st = check_routed(T, k, 1);
+  if (st != QGEMM_OK) return st;
+  if (E < 1 || E > QGEMM_MOE_MAX_EXPERTS) return QGEMM_ERR_SHAPE;
+  if (!bytes) return QGEMM_ERR_NULL;
+  *bytes = moe_sort_bytes(T * k, E);
+  return QGEMM_OK;
+}
+
+int qgemm_moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, const int32_t* experts, int k,
+                       int E, int32_t* offsets, int32_t* rows, void* xs, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!row_dtype(dtype)) return QGEMM_ERR_FORMAT;
+  const int st = check_routed(T, k, H);
+  if (st != QGEMM_OK) return st;
+  if (E < 1 || E > QGEMM_MOE_MAX_EXPERTS) return QGEMM_ERR_SHAPE;
+  if (!x || !experts || !offsets || !rows || !xs) return QGEMM_ERR_NULL;
+  if (!aligned16(x) || !aligned16(xs) || !aligned4(experts) || !aligned4(offsets) || !aligned4(rows))
+    return QGEMM_ERR_ALIGN;
+  const size_t need = moe_sort_bytes(T * k, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return QGEMM_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_moe_sort(experts, T * k, E, offsets, rows, static_cast<int*>(workspace), s);
+  if (e != cudaSuccess) return cuda_fail(e, "expert sort launch");
+  e = launch_moe_gather(x, T, H * (dtype == QGEMM_Y_BF16 ? 2 : 4), k, rows, xs, s);
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "row gather launch");
+}
+
+int qgemm_moe_dispatch_grad(const void* dxs, int dxs_dtype, int64_t T, int64_t H, const int32_t* rows,
+                            int k, void* dx, int dx_dtype, void* stream) {
+  if (!row_dtype(dxs_dtype) || !row_dtype(dx_dtype)) return QGEMM_ERR_FORMAT;
+  const int st = check_routed(T, k, H);
+  if (st != QGEMM_OK) return st;
+  if (!dxs || !rows || !dx) return QGEMM_ERR_NULL;
+  if (!aligned16(dxs) || !aligned16(dx) || !aligned4(rows)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaError_t e = launch_moe_combine(dxs_dtype == QGEMM_Y_BF16, dx_dtype == QGEMM_Y_BF16, dxs, T, H, k,
+                                           rows, nullptr, dx, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "dispatch gradient launch");
+}
+
+int qgemm_moe_combine(const void* ys, int ys_dtype, int64_t T, int64_t H, const int32_t* rows,
+                      const float* weights, int k, void* y, int y_dtype, void* stream) {
+  if (!row_dtype(ys_dtype) || !row_dtype(y_dtype)) return QGEMM_ERR_FORMAT;
+  const int st = check_routed(T, k, H);
+  if (st != QGEMM_OK) return st;
+  if (!ys || !rows || !weights || !y) return QGEMM_ERR_NULL;
+  if (!aligned16(ys) || !aligned16(y) || !aligned4(rows) || !aligned4(weights)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaError_t e = launch_moe_combine(ys_dtype == QGEMM_Y_BF16, y_dtype == QGEMM_Y_BF16, ys, T, H, k,
+                                           rows, weights, y, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "combine launch");
+}
+
+int qgemm_moe_combine_grad(const void* dy, int dy_dtype, const void* ys, int ys_dtype, int64_t T, int64_t H,
+                           const int32_t* rows, const float* weights, int k, void* dys, float* dweights,
+                           void* stream) {
+  if (!row_dtype(dy_dtype) || !row_dtype(ys_dtype)) return QGEMM_ERR_FORMAT;
+  const int st = check_routed(T, k, H);
+  if (st != QGEMM_OK) return st;
+  if (!dy || !ys || !rows || !weights || !dys || !dweights) return QGEMM_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(ys) || !aligned16(dys) || !aligned4(rows) || !aligned4(weights) ||
+      !aligned4(dweights))
+    return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaError_t e =
+      launch_moe_combine_grad(dy_dtype == QGEMM_Y_BF16, ys_dtype == QGEMM_Y_BF16, dy, ys, T, H, k, rows, weights,
+                              dys, dweights, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "combine gradient launch");
+}
+
+// ---------------------------------------------------------------------------------------
+// int8 weights and activations
+// ---------------------------------------------------------------------------------------
+namespace {
+int check_i8(int64_t N, int64_t K) {
+  const int st = check_fmt_shape(FMT_FP8, N, K);  // the same tile-major layout of byte codes
+  if (st != QGEMM_OK) return st;
+  return K > kI8MaxK ? QGEMM_ERR_SHAPE : QGEMM_OK;
+}
+// workspace: the codes and scales of the rows
+size_t i8_bytes(int64_t M, int64_t K, size_t* off_scales) {
+  const size_t codes = ((size_t)M * (size_t)K + 255) / 256 * 256;
+  if (off_scales) *off_scales = codes;
+  return codes + ((size_t)M * 4 + 255) / 256 * 256;
+}
+// quantise x, then the GEMM that `p` describes (its x operand is filled in here)
+int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  size_t off_s = 0;
+  const size_t need = i8_bytes(M, K, &off_s);
+  if (!workspace || workspace_bytes < need) return QGEMM_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  p.dev_err = error_word();
+  if (!p.dev_err) return cuda_fail(cudaGetLastError(), "cudaGetSymbolAddress");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t* xc = static_cast<int8_t*>(workspace);
+  float* xs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + off_s);
+  cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, xc, xs, s);
+  if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.chunks = (int)k_chunks(FMT_FP8, K);
+  p.xcodes = xc;
+  p.xscales = xs;
+  if (g_prof_begin) cudaEventRecord(g_prof_begin, s);
+  e = launch_i8_gemm(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, "int8 gemm launch");
+  if (g_prof_end) cudaEventRecord(g_prof_end, s);
+  return QGEMM_OK;
+}
+int check_i8_moe(const void* x, int64_t M, int64_t K, int E, const int32_t* off, int64_t max_rows, int64_t N) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  return check_moe(FMT_FP8, x, M, K, E, off, max_rows, N);
+}
+int check_i8_tables(const void* const* codes, const float* const* scales) {
+  if (!codes || !scales) return QGEMM_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(codes) & 7u) || (reinterpret_cast<uintptr_t>(scales) & 7u))
+    return QGEMM_ERR_ALIGN;
+  return QGEMM_OK;
+}
+}  // namespace
+
+int qgemm_i8_packed_size(int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  if (!code_bytes || !scale_bytes) return QGEMM_ERR_NULL;
+  *code_bytes = (size_t)packed_code_bytes(FMT_FP8, N, K);
+  *scale_bytes = (size_t)N * 4;
+  return QGEMM_OK;
+}
+
+int qgemm_i8_pack(const float* W, int64_t N, int64_t K, void* codes, float* scales, void* stream) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  if (!W || !codes || !scales) return QGEMM_ERR_NULL;
+  if (!aligned16(W) || !aligned16(codes) || !aligned4(scales)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaError_t e =
+      launch_i8_pack(W, N, K, static_cast<uint8_t*>(codes), scales, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "int8 pack launch");
+}
+
+int qgemm_i8_repack_rowmajor(int64_t N, int64_t K, const void* codes_rm, int64_t code_pitch, void* codes,
+                             void* stream) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  // the bytes move as FP8 codes do: one byte per element, no block scales
+  return qgemm_repack_rowmajor(QGEMM_FMT_FP8, N, K, codes_rm, code_pitch, nullptr, 0, codes, nullptr, stream);
+}
+
+int qgemm_i8_quant_x(const void* x, int64_t M, int64_t K, void* codes, float* scales, void* stream) {
+  const int st = check_i8(1, K);
+  if (st != QGEMM_OK) return st;
+  if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
+  if (!x || !codes || !scales) return QGEMM_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned4(scales)) return QGEMM_ERR_ALIGN;
+  if (!device_ok()) return QGEMM_ERR_DEVICE;
+  const cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, static_cast<int8_t*>(codes), scales,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "int8 quantisation launch");
+}
+
+int qgemm_i8_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
+  if (!bytes) return QGEMM_ERR_NULL;
+  *bytes = i8_bytes(M, K, nullptr);
+  return QGEMM_OK;
+}
+
+int qgemm_i8_run(const void* x, int64_t M, int64_t K, const void* codes, const float* scales, int64_t N, void* y,
+                 int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
+  if (!row_dtype(y_dtype)) return QGEMM_ERR_FORMAT;
+  if (!x || !codes || !scales || !y) return QGEMM_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(y) || !aligned4(scales)) return QGEMM_ERR_ALIGN;
+  I8Params p{};
+  p.nmat = 1;
+  p.codes[0] = static_cast<const uint8_t*>(codes);
+  p.scales[0] = scales;
+  p.out = y;
+  p.out_bf16 = y_dtype == QGEMM_Y_BF16;
+  return i8_run_impl(x, M, K, N, p, workspace, workspace_bytes, stream);
+}
+
+int qgemm_i8_moe_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) {
+  const int st = check_i8(N, K);
+  if (st != QGEMM_OK) return st;
+  if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
+  if (!bytes) return QGEMM_ERR_NULL;
+  *bytes = i8_bytes(M, K, nullptr);
+  return QGEMM_OK;
+}
+
+int qgemm_i8_moe_run(const void* x, int64_t M, int64_t K, int E, const int32_t* off, int64_t max_rows,
+                     const void* const* codes_tab, const float* const* scales_tab, int64_t N, void* y, int y_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_i8_moe(x, M, K, E, off, max_rows, N);
+  if (st != QGEMM_OK) return st;
+  if (!row_dtype(y_dtype)) return QGEMM_ERR_FORMAT;
+  if (!y) return QGEMM_ERR_NULL;
+  if (!aligned16(y)) return QGEMM_ERR_ALIGN;
+  st = check_i8_tables(codes_tab, scales_tab);
+  if (st != QGEMM_OK) return st;
+  I8Params p{};
+  p.nmat = 1;
+  p.off = off;
+  p.E = E;
+  p.max_rows = (int)max_rows;
+  p.codes_tab[0] = reinterpret_cast<const uint8_t* const*>(codes_tab);
+  p.scales_tab[0] = scales_tab;
+  p.out = y;
+  p.out_bf16 = y_dtype == QGEMM_Y_BF16;
+  return i8_run_impl(x, M, K, N, p, workspace, workspace_bytes, stream);
+}
+
+int qgemm_i8_moe_gate_up(const void* x, int64_t M, int64_t K, int E, const int32_t* off, int64_t max_rows,
+                         const void* const* g_codes_tab, const float* const* g_scales_tab,
+                         const void* const* u_codes_tab, const float* const* u_scales_tab, int64_t N, void* h,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_i8_moe(x, M, K, E, off, max_rows, N);
+  if (st != QGEMM_OK) return st;
+  if (!h) return QGEMM_ERR_NULL;
+  if (!aligned16(h)) return QGEMM_ERR_ALIGN;
+  st = check_i8_tables(g_codes_tab, g_scales_tab);
+  if (st == QGEMM_OK) st = check_i8_tables(u_codes_tab, u_scales_tab);
+  if (st != QGEMM_OK) return st;
+  I8Params p{};
+  p.nmat = 2;
+  p.off = off;
+  p.E = E;
+  p.max_rows = (int)max_rows;
+  p.codes_tab[0] = reinterpret_cast<const uint8_t* const*>(g_codes_tab);
+  p.codes_tab[1] = reinterpret_cast<const uint8_t* const*>(u_codes_tab);
+  p.scales_tab[0] = g_scales_tab;
+  p.scales_tab[1] = u_scales_tab;
+  p.out = h;
+  p.out_bf16 = 1;
+  return i8_run_impl(x, M, K, N, p, workspace, workspace_bytes, stream);
 }
 
 int qgemm_profile_events(void* begin_event, void* end_event) {

@@ -7,6 +7,7 @@ missing or fails to load, the call raises -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -57,6 +58,22 @@ SIGNATURES = [
     ("qgemm_bs_run", _I, [_I, _VP, _I64, _I64, _VP, _VP, _VP, _I64, _VP, _I, _VP, _SZ, _VP]),
     ("qgemm_bs_ffn_workspace_size", _I, [_I, _I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     ("qgemm_bs_ffn_gate_up", _I, [_I, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP,
+                                  _VP, _SZ, _VP]),
+    ("qgemm_moe_dispatch_workspace_size", _I, [_I64, _I, _I, ctypes.POINTER(_SZ)]),
+    ("qgemm_moe_dispatch", _I, [_VP, _I, _I64, _I64, _VP, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    ("qgemm_moe_dispatch_grad", _I, [_VP, _I, _I64, _I64, _VP, _I, _VP, _I, _VP]),
+    ("qgemm_moe_combine", _I, [_VP, _I, _I64, _I64, _VP, _VP, _I, _VP, _I, _VP]),
+    ("qgemm_moe_combine_grad", _I, [_VP, _I, _VP, _I, _I64, _I64, _VP, _VP, _I, _VP, _VP, _VP]),
+    ("qgemm_i8_packed_size", _I, [_I64, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    ("qgemm_i8_pack", _I, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    ("qgemm_i8_repack_rowmajor", _I, [_I64, _I64, _VP, _I64, _VP, _VP]),
+    ("qgemm_i8_quant_x", _I, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    ("qgemm_i8_workspace_size", _I, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    ("qgemm_i8_run", _I, [_VP, _I64, _I64, _VP, _VP, _I64, _VP, _I, _VP, _SZ, _VP]),
+    ("qgemm_i8_moe_workspace_size", _I, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    ("qgemm_i8_moe_run", _I, [_VP, _I64, _I64, _I, _VP, _I64, _VP, _VP, _I64, _VP, _I, _VP, _SZ,
+                              _VP]),
+    ("qgemm_i8_moe_gate_up", _I, [_VP, _I64, _I64, _I, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _VP,
                                   _VP, _SZ, _VP]),
     ("qgemm_split_k", _I, [_I, _I64, _I64, ctypes.POINTER(_I)]),
     ("qgemm_device_status", _I, [_I]),
@@ -391,4 +408,272 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
                                    _ptr(up.codes), _ptr(up.scales), _ptr(up.ts), gate.N, _ptr(h),
                                    _ptr(workspace), workspace.numel(), _stream(stream)),
            "qgemm_moe_gate_up")
+    return h
+
+
+# ---- routed tokens: sorted by expert, and back --------------------------------------------
+
+_ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
+
+
+def _on(*tensors):
+    """The checks every tensor of a routed or int8 call passes: on one CUDA device, contiguous.
+    Returns that device's guard (the library launches on the current device)."""
+    dev = tensors[0].device
+    for t in tensors:
+        assert t.device == dev and t.is_contiguous()
+    assert dev.type == "cuda"
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NOTHING
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def _scratch(nbytes: int, device, stream):
+    """Device bytes for one call on `stream`, held until the call's work there is done."""
+    t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def moe_dispatch_workspace_size(T: int, k: int, E: int) -> int:
+    b = _SZ()
+    _check(lib().qgemm_moe_dispatch_workspace_size(T, k, E, ctypes.byref(b)),
+           "qgemm_moe_dispatch_workspace_size")
+    return b.value
+
+
+def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tensor | None = None,
+                 offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
+                 workspace=None, stream=None):
+    """qgemm_moe_dispatch: tokens x [T, H] (bf16 or fp32) and their experts int32 [T, k] (outside
+    [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
+    assert x.dtype in _ROW_DTYPES and x.dim() == 2
+    assert experts.dtype == torch.int32 and experts.dim() == 2 and experts.shape[0] == x.shape[0]
+    T, H = x.shape
+    k = experts.shape[1]
+    if xs is None:
+        xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+    if rows is None:
+        rows = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    assert xs.dtype == x.dtype and xs.shape == (T * k, H)
+    assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
+    assert rows.dtype == torch.int32 and rows.shape == (T, k)
+    if workspace is None:
+        nbytes = moe_dispatch_workspace_size(T, k, E)
+        workspace = _scratch(nbytes, x.device, stream)
+    with _on(x, experts, xs, offsets, rows, workspace):
+        _check(lib().qgemm_moe_dispatch(_ptr(x), _ROW_DTYPES[x.dtype], T, H, _ptr(experts), k, E,
+                                        _ptr(offsets), _ptr(rows), _ptr(xs), _ptr(workspace),
+                                        _nbytes(workspace), _stream(stream)), "qgemm_moe_dispatch")
+    return xs, offsets, rows
+
+
+def _routed(a, rows):
+    assert a.dtype in _ROW_DTYPES and a.dim() == 2
+    assert rows.dtype == torch.int32 and rows.dim() == 2 and a.shape[0] == rows.numel()
+    return rows.shape[0], rows.shape[1], a.shape[1]
+
+
+def _routed_out(out, shape, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    assert out.dtype in _ROW_DTYPES and out.shape == shape
+    return out
+
+
+def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | None = None,
+                      dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
+    T, k, H = _routed(dxs, rows)
+    dx = _routed_out(dx, (T, H), dx_dtype, dxs.device)
+    with _on(dxs, rows, dx):
+        _check(lib().qgemm_moe_dispatch_grad(_ptr(dxs), _ROW_DTYPES[dxs.dtype], T, H, _ptr(rows), k,
+                                             _ptr(dx), _ROW_DTYPES[dx.dtype], _stream(stream)),
+               "qgemm_moe_dispatch_grad")
+    return dx
+
+
+def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
+                y: torch.Tensor | None = None, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """qgemm_moe_combine: y[t] = sum_j weights[t, j] * ys[rows[t, j]], weights fp32 [T, k]."""
+    T, k, H = _routed(ys, rows)
+    assert weights.dtype == torch.float32 and weights.shape == rows.shape
+    y = _routed_out(y, (T, H), y_dtype, ys.device)
+    with _on(ys, rows, weights, y):
+        _check(lib().qgemm_moe_combine(_ptr(ys), _ROW_DTYPES[ys.dtype], T, H, _ptr(rows),
+                                       _ptr(weights), k, _ptr(y), _ROW_DTYPES[y.dtype],
+                                       _stream(stream)), "qgemm_moe_combine")
+    return y
+
+
+def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
+                     dys: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
+    """qgemm_moe_combine_grad: the gradients (dys [T*k, H] in ys's type, dw fp32 [T, k]) of
+    moe_combine, given dy [T, H]."""
+    T, k, H = _routed(ys, rows)
+    assert weights.dtype == torch.float32 and weights.shape == rows.shape
+    assert dy.dtype in _ROW_DTYPES and dy.shape == (T, H)
+    dys = _routed_out(dys, (T * k, H), ys.dtype, ys.device)
+    assert dys.dtype == ys.dtype
+    if dw is None:
+        dw = torch.empty((T, k), dtype=torch.float32, device=ys.device)
+    assert dw.dtype == torch.float32 and dw.shape == rows.shape
+    with _on(dy, ys, rows, weights, dys, dw):
+        _check(lib().qgemm_moe_combine_grad(_ptr(dy), _ROW_DTYPES[dy.dtype], _ptr(ys),
+                                            _ROW_DTYPES[ys.dtype], T, H, _ptr(rows), _ptr(weights),
+                                            k, _ptr(dys), _ptr(dw), _stream(stream)),
+               "qgemm_moe_combine_grad")
+    return dys, dw
+
+
+# ---- int8 weights and activations ---------------------------------------------------------
+
+def i8_packed_size(N: int, K: int):
+    cb, sb = _SZ(), _SZ()
+    _check(lib().qgemm_i8_packed_size(N, K, ctypes.byref(cb), ctypes.byref(sb)), "qgemm_i8_packed_size")
+    return cb.value, sb.value
+
+
+class I8Weight:
+    """Device buffers of one int8 [N, K] matrix: tile-major codes, fp32 scales [N]."""
+
+    def __init__(self, N: int, K: int, device=None):
+        self.N, self.K = N, K
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        self.codes = torch.empty(i8_packed_size(N, K)[0], dtype=torch.uint8, device=device)
+        self.scales = torch.empty(N, dtype=torch.float32, device=device)
+
+    @property
+    def nbytes(self) -> int:
+        """Algorithmic bytes a GEMM reads for this matrix (codes + scales, no padding)."""
+        return self.N * self.K + 4 * self.N
+
+
+def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weight:
+    """qgemm_i8_pack: W fp32 [N, K] on the device -> I8Weight."""
+    assert W.dtype == torch.float32 and W.dim() == 2
+    N, K = W.shape
+    w = out or I8Weight(N, K, W.device)
+    assert (w.N, w.K) == (N, K)
+    with _on(W, w.codes, w.scales):
+        _check(lib().qgemm_i8_pack(_ptr(W), N, K, _ptr(w.codes), _ptr(w.scales), _stream(stream)),
+               "qgemm_i8_pack")
+    return w
+
+
+def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weight | None = None,
+                       stream=None) -> I8Weight:
+    """qgemm_i8_repack_rowmajor: a checkpoint's int8 codes [N, K] (rows may be strided) and fp32
+    scales [N] -> I8Weight.  The scales are kept, not copied."""
+    assert codes_rm.dtype == torch.int8 and codes_rm.dim() == 2 and codes_rm.stride(1) == 1
+    N, K = codes_rm.shape
+    assert scales.dtype == torch.float32 and scales.shape == (N,)
+    w = out or I8Weight(N, K, codes_rm.device)
+    assert (w.N, w.K) == (N, K)
+    w.scales = scales
+    with _on(w.codes, scales):
+        assert codes_rm.device == scales.device
+        _check(lib().qgemm_i8_repack_rowmajor(N, K, _ptr(codes_rm), codes_rm.stride(0), _ptr(w.codes),
+                                              _stream(stream)), "qgemm_i8_repack_rowmajor")
+    return w
+
+
+def i8_quant_x(x: torch.Tensor, stream=None):
+    """qgemm_i8_quant_x: x bf16 [M, K] -> (codes int8 [M, K], scales fp32 [M])."""
+    assert x.dtype == torch.bfloat16 and x.dim() == 2
+    M, K = x.shape
+    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    with _on(x, codes, scales):
+        _check(lib().qgemm_i8_quant_x(_ptr(x), M, K, _ptr(codes), _ptr(scales), _stream(stream)),
+               "qgemm_i8_quant_x")
+    return codes, scales
+
+
+def i8_workspace_size(N: int, K: int, M: int) -> int:
+    b = _SZ()
+    _check(lib().qgemm_i8_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_workspace_size")
+    return b.value
+
+
+def _i8_y(y, M, N, y_dtype, device):
+    if y is None:
+        y = torch.empty((M, N), dtype=y_dtype, device=device)
+    assert y.dtype in _ROW_DTYPES and y.shape == (M, N)
+    return y
+
+
+def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=torch.float32,
+           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """qgemm_i8_run: x bf16 [M, K], quantised per row on the fly -> y [M, N] (fp32 or bf16)."""
+    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == w.K
+    M, K = x.shape
+    y = _i8_y(y, M, w.N, y_dtype, x.device)
+    if workspace is None:
+        workspace = _scratch(i8_workspace_size(w.N, K, M), x.device, stream)
+    with _on(x, w.codes, w.scales, y, workspace):
+        _check(lib().qgemm_i8_run(_ptr(x), M, K, _ptr(w.codes), _ptr(w.scales), w.N, _ptr(y),
+                                  _ROW_DTYPES[y.dtype], _ptr(workspace), _nbytes(workspace),
+                                  _stream(stream)), "qgemm_i8_run")
+    return y
+
+
+class I8ExpertTable:
+    """Device pointer tables of a list of int8 experts (one I8Weight each, same shape)."""
+
+    def __init__(self, experts):
+        assert experts and all((e.N, e.K) == (experts[0].N, experts[0].K) and
+                               e.codes.device == experts[0].codes.device for e in experts)
+        self.N, self.K, self.E = experts[0].N, experts[0].K, len(experts)
+        dev = experts[0].codes.device
+        self.codes = torch.tensor([e.codes.data_ptr() for e in experts], dtype=torch.int64, device=dev)
+        self.scales = torch.tensor([e.scales.data_ptr() for e in experts], dtype=torch.int64, device=dev)
+        self.experts = experts  # keeps the buffers alive
+
+
+def i8_moe_workspace_size(N: int, K: int, M: int) -> int:
+    b = _SZ()
+    _check(lib().qgemm_i8_moe_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_moe_workspace_size")
+    return b.value
+
+
+def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_rows: int,
+               y: torch.Tensor | None = None, y_dtype=torch.float32, workspace=None, stream=None):
+    """qgemm_i8_moe_run: rows of x grouped by expert (int32 offsets[E+1] on the device)."""
+    _moe_common(x, offsets, tab)
+    M, K = x.shape
+    y = _i8_y(y, M, tab.N, y_dtype, x.device)
+    if workspace is None:
+        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x.device, stream)
+    with _on(x, offsets, tab.codes, y, workspace):
+        _check(lib().qgemm_i8_moe_run(_ptr(x), M, K, tab.E, _ptr(offsets), max_rows, _ptr(tab.codes),
+                                      _ptr(tab.scales), tab.N, _ptr(y), _ROW_DTYPES[y.dtype],
+                                      _ptr(workspace), _nbytes(workspace), _stream(stream)),
+               "qgemm_i8_moe_run")
+    return y
+
+
+def i8_moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: I8ExpertTable, up: I8ExpertTable,
+                   max_rows: int, h: torch.Tensor | None = None, workspace=None, stream=None):
+    """qgemm_i8_moe_gate_up: h = bf16(SiLU(g) * u) per routed row."""
+    _moe_common(x, offsets, gate)
+    assert (gate.N, gate.K, gate.E) == (up.N, up.K, up.E)
+    M, K = x.shape
+    h = _i8_y(h, M, gate.N, torch.bfloat16, x.device)
+    assert h.dtype == torch.bfloat16
+    if workspace is None:
+        workspace = _scratch(i8_moe_workspace_size(gate.N, K, M), x.device, stream)
+    with _on(x, offsets, gate.codes, up.codes, h, workspace):
+        _check(lib().qgemm_i8_moe_gate_up(_ptr(x), M, K, gate.E, _ptr(offsets), max_rows,
+                                          _ptr(gate.codes), _ptr(gate.scales), _ptr(up.codes),
+                                          _ptr(up.scales), gate.N, _ptr(h), _ptr(workspace),
+                                          _nbytes(workspace), _stream(stream)), "qgemm_i8_moe_gate_up")
     return h

@@ -327,6 +327,102 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Routed tokens: the rows the qgemm_moe_* entry points read, sorted by expert, and the way back
+ * with the routing weights applied, each with its gradient (Strix Halo prefill journey, the
+ * routed MoE around the expert kernels).  T tokens choose k experts each: slot (t, j), in the order
+ * t k + j, belongs to expert experts_dev[t][j].  A slot whose expert lies outside [0, E) (-1 for
+ * a padded token) belongs to none: it has no row and adds nothing.  A token may name an expert
+ * more than once.  T k <= 2^31-1, 1 <= E <= QGEMM_MOE_MAX_EXPERTS, H >= 1 elements per row, of
+ * type QGEMM_Y_F32 or QGEMM_Y_BF16; int32 and weight arrays need 4-byte alignment, rows 16.
+ * Buffers written must not overlap buffers read.  Sums run in fp32 in a fixed order and round
+ * once; equal inputs give equal bits.
+ *
+ * qgemm_moe_dispatch writes
+ *   rows_dev    int32 [T][k]: the slot's row among the sorted rows -- experts ascending, slots
+ *               in order within an expert -- or -1;
+ *   offsets_dev int32 [E+1]: rows offsets[e] .. offsets[e+1]-1 belong to expert e (the offsets
+ *               of qgemm_moe_run; offsets[E] slots have a row);
+ *   xs_dev      [T k][H]: xs[rows[t][j]] = x[t] bit for bit.  Rows from offsets[E] on are left as
+ *               they were.
+ * Workspace: qgemm_moe_dispatch_workspace_size() bytes, no initialisation.
+ *
+ * qgemm_moe_combine:       y[t] = sum_j weights[t][j] * ys[rows[t][j]], j ascending.
+ * qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t][j]] (the gradient of x given that of xs).
+ * qgemm_moe_combine_grad:  dys[rows[t][j]] = weights[t][j] * dy[t] (in ys's type; rows no slot
+ *   names are left as they were) and dweights[t][j] = sum_h dy[t][h] ys[rows[t][j]][h] (0
+ *   without a row).
+ * ys, dys, dxs hold T k rows; a value of rows_dev outside [0, T k) counts as -1, and no two slots
+ * may name one row in qgemm_moe_combine_grad.  A slot without a row is not read: what its weight
+ * or a row behind the last expert holds, NaN included, reaches no output.
+ * Errors: QGEMM_ERR_FORMAT (types), _SHAPE, _NULL, _ALIGN, _WORKSPACE, _DEVICE, _CUDA.
+ */
+#define QGEMM_MOE_MAX_EXPERTS 4096
+
+int qgemm_moe_dispatch_workspace_size(int64_t T, int k, int E, size_t* bytes);
+int qgemm_moe_dispatch(const void* x_dev, int dtype, int64_t T, int64_t H,
+                       const int32_t* experts_dev, int k, int E, int32_t* offsets_dev,
+                       int32_t* rows_dev, void* xs_dev, void* workspace, size_t workspace_bytes,
+                       void* stream);
+int qgemm_moe_dispatch_grad(const void* dxs_dev, int dxs_dtype, int64_t T, int64_t H,
+                            const int32_t* rows_dev, int k, void* dx_dev, int dx_dtype,
+                            void* stream);
+int qgemm_moe_combine(const void* ys_dev, int ys_dtype, int64_t T, int64_t H,
+                      const int32_t* rows_dev, const float* weights_dev, int k, void* y_dev,
+                      int y_dtype, void* stream);
+int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev, int ys_dtype,
+                           int64_t T, int64_t H, const int32_t* rows_dev,
+                           const float* weights_dev, int k, void* dys_dev, float* dweights_dev,
+                           void* stream);
+
+/*
+ * int8 weights with one fp32 scale per output channel, times bf16 rows quantised to int8 with one
+ * scale per row on the fly (W8A8; the pages' W8A8 int8 MMA tiers):
+ *   sx[m] = fp32_RNE(max|x_m| / 127),  q[m][k] = RNE(x[m][k] / sx[m])  (ties to even, of the
+ *           exact quotient); a zero row gets sx = 0 and q = 0; a row that holds an infinity or
+ *           NaN gets sx = NaN and q = 0, so that its row of y is NaN and no other row is touched;
+ *   y[m][n] = fp32(sum_k q[m][k] p[n][k]) * sw[n] * sx[m], fp32 products in this order.
+ * The sum is exact in int32, so a row of y is the same at any M and beside any other rows.
+ * K: a multiple of 16 (QGEMM_ERR_K_BLOCK) and at most 131072 (QGEMM_ERR_SHAPE), which keeps the
+ * sum inside int32 for codes of -128 .. 127.
+ * Packed weights: codes in the tile-major layout of one-byte codes above (CK = 128), scales
+ * float [N].  qgemm_i8_pack quantises fp32 W the same way per channel; qgemm_i8_repack_rowmajor
+ * brings int8 codes [N][code_pitch] of a checkpoint into the layout (its scales are used as
+ * they are).  qgemm_i8_quant_x is the row quantisation alone: codes int8 [M][K], scales [M].
+ * Workspaces hold the codes and scales of x.  Scales need 4-byte alignment, all else 16.
+ * Errors as for qgemm_run.
+ */
+int qgemm_i8_packed_size(int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes);
+int qgemm_i8_pack(const float* W_dev, int64_t N, int64_t K, void* codes_dev, float* scales_dev,
+                  void* stream);
+int qgemm_i8_repack_rowmajor(int64_t N, int64_t K, const void* codes_rm_dev, int64_t code_pitch,
+                             void* codes_dev, void* stream);
+int qgemm_i8_quant_x(const void* x_dev, int64_t M, int64_t K, void* codes_dev, float* scales_dev,
+                     void* stream);
+int qgemm_i8_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes);
+int qgemm_i8_run(const void* x_dev, int64_t M, int64_t K, const void* codes_dev,
+                 const float* scales_dev, int64_t N, void* y_dev, int y_dtype, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * The routed forms, with rows grouped by expert, pointer tables, max_rows and refusal of bad
+ * table entries as for qgemm_moe_run and qgemm_moe_gate_up (the tables hold each expert's codes,
+ * 16-byte aligned, and scales, 4-byte aligned).  Rows no expert owns are left as they were.
+ *   qgemm_i8_moe_run:     y[m] = the product above with row m's expert.
+ *   qgemm_i8_moe_gate_up: h[m] = bf16_RNE(SiLU(g) * u), g and u fp32 as y above.
+ */
+int qgemm_i8_moe_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes);
+int qgemm_i8_moe_run(const void* x_dev, int64_t M, int64_t K, int E, const int32_t* offsets_dev,
+                     int64_t max_rows, const void* const* codes_tab_dev,
+                     const float* const* scales_tab_dev, int64_t N, void* y_dev, int y_dtype,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int qgemm_i8_moe_gate_up(const void* x_dev, int64_t M, int64_t K, int E,
+                         const int32_t* offsets_dev, int64_t max_rows,
+                         const void* const* g_codes_tab_dev, const float* const* g_scales_tab_dev,
+                         const void* const* u_codes_tab_dev, const float* const* u_scales_tab_dev,
+                         int64_t N, void* h_dev, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
  * Number of K splits qgemm_run uses for 1 <= B <= 256 (a function of fmt, N, K only).
  */
 int qgemm_split_k(int fmt, int64_t N, int64_t K, int* splits);
