@@ -47,7 +47,6 @@ cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes,
                            cudaStream_t stream);
 cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales,
                             cudaStream_t stream);
-cudaError_t launch_i8_gemm(const I8Params& p, cudaStream_t stream);
 int* device_error_word();
 }  // namespace qg
 
@@ -368,6 +367,26 @@ bool x_map(CUtensorMap* out, int dev, CUtensorMapDataType dt, const void* base, 
                       : make_map(out, dt, 2, base, (uint64_t)K, (uint64_t)rows,
                                  (uint64_t)pitch * 2, kSubK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return false;
+  const int i = g_maps.next;
+  g_maps.key[i] = k;
+  g_maps.map[i] = *out;
+  g_maps.next = (i + 1) % kCacheEntries;
+  if (g_maps.used < kCacheEntries) ++g_maps.used;
+  return true;
+}
+
+// int8 rows: 2-D map {K, rows} of bytes, boxes of 128 x box_rows in the 128-byte swizzle (bytes
+// and rows past the end read zeros).
+bool i8_x_map(CUtensorMap* out, int dev, const void* base, int64_t rows, int64_t K, uint32_t box_rows) {
+  const MapKey k{dev, (int)CU_TENSOR_MAP_DATA_TYPE_UINT8, 0, base, rows, K, K, box_rows, 1};
+  for (int i = 0; i < g_maps.used; ++i)
+    if (g_maps.key[i] == k) {
+      *out = g_maps.map[i];
+      return true;
+    }
+  if (!make_map(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, (uint64_t)K, (uint64_t)rows, (uint64_t)K, 128,
+                box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
+    return false;
   const int i = g_maps.next;
   g_maps.key[i] = k;
   g_maps.map[i] = *out;
@@ -1180,35 +1199,50 @@ int check_i8(int64_t N, int64_t K) {
   if (st != QGEMM_OK) return st;
   return K > kI8MaxK ? QGEMM_ERR_SHAPE : QGEMM_OK;
 }
-// workspace: the codes and scales of the rows
-size_t i8_bytes(int64_t M, int64_t K, size_t* off_scales) {
-  const size_t codes = ((size_t)M * (size_t)K + 255) / 256 * 256;
-  if (off_scales) *off_scales = codes;
-  return codes + ((size_t)M * 4 + 255) / 256 * 256;
+// workspace: the codes and scales of the rows, then a plain call's split-K partials
+struct I8Ws {
+  size_t scales, partials, total;
+};
+I8Ws i8_ws(int64_t N, int64_t K, int64_t M, bool routed) {
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  I8Ws w;
+  w.scales = up((size_t)M * (size_t)K);
+  w.partials = w.scales + up((size_t)M * 4);
+  w.total = w.partials + (routed ? 0 : up(i8_partial_bytes(N, K, M)));
+  return w;
 }
-// quantise x, then the GEMM that `p` describes (its x operand is filled in here)
+// quantise x, then the GEMM that `p` describes (its x operand and tiling are filled in here)
 int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, void* workspace,
                 size_t workspace_bytes, void* stream) {
-  size_t off_s = 0;
-  const size_t need = i8_bytes(M, K, &off_s);
-  if (!workspace || workspace_bytes < need) return QGEMM_ERR_WORKSPACE;
+  const bool routed = p.off != nullptr;
+  const I8Ws w = i8_ws(N, K, M, routed);
+  if (!workspace || workspace_bytes < w.total) return QGEMM_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QGEMM_ERR_ALIGN;
   if (!device_ok()) return QGEMM_ERR_DEVICE;
   p.dev_err = error_word();
   if (!p.dev_err) return cuda_fail(cudaGetLastError(), "cudaGetSymbolAddress");
+  int dev = 0;
+  const int st = current_device(&dev);
+  if (st != QGEMM_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int8_t* xc = static_cast<int8_t*>(workspace);
-  float* xs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + off_s);
-  cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, xc, xs, s);
-  if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
+  uint8_t* wsb = static_cast<uint8_t*>(workspace);
+  i8_plan(N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, routed, &p);
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.chunks = (int)k_chunks(FMT_FP8, K);
-  p.xcodes = xc;
-  p.xscales = xs;
+  p.xcodes = reinterpret_cast<const int8_t*>(wsb);
+  p.xscales = reinterpret_cast<const float*>(wsb + w.scales);
+  p.ws = reinterpret_cast<int*>(wsb + w.partials);
+  CUtensorMap map;
+  if (!i8_x_map(&map, dev, wsb, M, K, (uint32_t)p.box)) {
+    snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled failed");
+    return QGEMM_ERR_CUDA;
+  }
+  cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, reinterpret_cast<int8_t*>(wsb),
+                                  reinterpret_cast<float*>(wsb + w.scales), s);
+  if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
   if (g_prof_begin) cudaEventRecord(g_prof_begin, s);
-  e = launch_i8_gemm(p, s);
+  e = launch_i8_gemm(p, map, s);
   if (e != cudaSuccess) return cuda_fail(e, "int8 gemm launch");
   if (g_prof_end) cudaEventRecord(g_prof_end, s);
   return QGEMM_OK;
@@ -1216,6 +1250,7 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
 int check_i8_moe(const void* x, int64_t M, int64_t K, int E, const int32_t* off, int64_t max_rows, int64_t N) {
   const int st = check_i8(N, K);
   if (st != QGEMM_OK) return st;
+  if (E > QGEMM_MOE_MAX_EXPERTS) return QGEMM_ERR_SHAPE;
   return check_moe(FMT_FP8, x, M, K, E, off, max_rows, N);
 }
 int check_i8_tables(const void* const* codes, const float* const* scales) {
@@ -1271,7 +1306,7 @@ int qgemm_i8_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) {
   if (st != QGEMM_OK) return st;
   if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
   if (!bytes) return QGEMM_ERR_NULL;
-  *bytes = i8_bytes(M, K, nullptr);
+  *bytes = i8_ws(N, K, M, false).total;
   return QGEMM_OK;
 }
 
@@ -1297,7 +1332,7 @@ int qgemm_i8_moe_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) 
   if (st != QGEMM_OK) return st;
   if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
   if (!bytes) return QGEMM_ERR_NULL;
-  *bytes = i8_bytes(M, K, nullptr);
+  *bytes = i8_ws(N, K, M, true).total;
   return QGEMM_OK;
 }
 

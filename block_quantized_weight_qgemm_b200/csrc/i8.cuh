@@ -1,10 +1,12 @@
 // i8.cuh -- parameters of the int8 GEMM, shared by its kernels and the host layer.
 #pragma once
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <cstdint>
 
 namespace qg {
 
+constexpr int kI8SMs = 148;  // of a B200, for the rules that weigh tilings
 constexpr int64_t kI8MaxK = 131072;  // |sum| <= K * 128 * 127 stays inside int32
 
 struct I8Params {
@@ -23,6 +25,19 @@ struct I8Params {
   int E, max_rows;
   const uint8_t* const* codes_tab[2];
   const float* const* scales_tab[2];
+  // Tiling (i8_plan)
+  int tiles;        // 128-channel tiles
+  int NB;           // rows of x per unit at most (MMA N), a multiple of 16
+  int box;          // rows per TMA box
+  int b_tiles;      // row tiles of a plain call (routed: of an expert, at most)
+  int S;            // K ranges; above 1 the kernel writes int32 partials to ws
+  int units, stages, stage_bytes, tmem_cols;
+  int w_again;      // a weight tile is read by more than one unit
+  int* ws;          // [S][M][N]
 };
+
+void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params* p);
+size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M);
+cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map, cudaStream_t stream);
 
 }  // namespace qg

@@ -377,8 +377,8 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
 /*
  * int8 weights with one fp32 scale per output channel, times bf16 rows quantised to int8 with one
  * scale per row on the fly (W8A8; the pages' W8A8 int8 MMA tiers):
- *   sx[m] = fp32_RNE(max|x_m| / 127),  q[m][k] = RNE(x[m][k] / sx[m])  (ties to even, of the
- *           exact quotient); a zero row gets sx = 0 and q = 0; a row that holds an infinity or
+ *   sx[m] = fp32_RNE(max|x_m| * fp32_RNE(1/127)),  q[m][k] = RNE(x[m][k] / sx[m])  (ties to
+ *           even, of the exact quotient); a zero row gets sx = 0 and q = 0; a row that holds an infinity or
  *           NaN gets sx = NaN and q = 0, so that its row of y is NaN and no other row is touched;
  *   y[m][n] = fp32(sum_k q[m][k] p[n][k]) * sw[n] * sx[m], fp32 products in this order.
  * The sum is exact in int32, so a row of y is the same at any M and beside any other rows.
@@ -388,7 +388,7 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
  * float [N].  qgemm_i8_pack quantises fp32 W the same way per channel; qgemm_i8_repack_rowmajor
  * brings int8 codes [N][code_pitch] of a checkpoint into the layout (its scales are used as
  * they are).  qgemm_i8_quant_x is the row quantisation alone: codes int8 [M][K], scales [M].
- * Workspaces hold the codes and scales of x.  Scales need 4-byte alignment, all else 16.
+ * Workspaces hold the codes and scales of x and, where K is split, int32 partials.  Scales need 4-byte alignment, all else 16.
  * Errors as for qgemm_run.
  */
 int qgemm_i8_packed_size(int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes);
@@ -406,7 +406,8 @@ int qgemm_i8_run(const void* x_dev, int64_t M, int64_t K, const void* codes_dev,
 /*
  * The routed forms, with rows grouped by expert, pointer tables, max_rows and refusal of bad
  * table entries as for qgemm_moe_run and qgemm_moe_gate_up (the tables hold each expert's codes,
- * 16-byte aligned, and scales, 4-byte aligned).  Rows no expert owns are left as they were.
+ * 16-byte aligned, and scales, 4-byte aligned; E <= QGEMM_MOE_MAX_EXPERTS).  Rows no expert
+ * owns are left as they were.
  *   qgemm_i8_moe_run:     y[m] = the product above with row m's expert.
  *   qgemm_i8_moe_gate_up: h[m] = bf16_RNE(SiLU(g) * u), g and u fp32 as y above.
  */

@@ -32,7 +32,7 @@ def half(dtype):
 def quantise(a):
     """(codes float64, scales float32) of the rows of a finite array, by the definition."""
     a = a.double()
-    s = a.abs().amax(1).float() / 127.0
+    s = a.abs().amax(1).float() * (torch.ones(()) / 127)
     q = torch.round(a / torch.where(s > 0, s, torch.ones_like(s)).double()[:, None])
     return q.clamp(-127, 127), s
 
@@ -190,7 +190,7 @@ def test_largest_sum_is_exact():
     y = qgemm.i8_run(x.cuda(), w).cpu().double()
     sums = torch.tensor([[-128.0] * 130, [128.0] * 130, [0.0] * 130]).double() * 127 * K
     sums[0, 1], sums[1, 1] = 127.0 * 127 * K, -127.0 * 127 * K
-    s = float(torch.tensor(1.0) / 127)
+    s = float(torch.ones(()) / 127)
     assert ((y - sums * s).abs() <= 3 * U * (sums * s).abs()).all()
 
 

@@ -75,7 +75,7 @@ REFUSED = [
     (_run, dict(y=None), NULL), (_run, dict(x=8), ALIGN), (_run, dict(c=8), ALIGN),
     (_run, dict(y=8), ALIGN), (_run, dict(s=18), ALIGN), (_run, dict(ws=None), WORKSPACE),
     (_run, dict(n=255), WORKSPACE), (_run, dict(ws=24), ALIGN),
-    (_moe, dict(M=0), SHAPE), (_moe, dict(E=0), SHAPE), (_moe, dict(mr=0), SHAPE),
+    (_moe, dict(M=0), SHAPE), (_moe, dict(E=0), SHAPE), (_moe, dict(E=4097), SHAPE), (_moe, dict(mr=0), SHAPE),
     (_moe, dict(K=131088), SHAPE), (_moe, dict(K=24), K_BLOCK), (_moe, dict(ydt=2), FORMAT),
     (_moe, dict(x=None), NULL), (_moe, dict(off=None), NULL), (_moe, dict(c=None), NULL),
     (_moe, dict(s=None), NULL), (_moe, dict(y=None), NULL), (_moe, dict(off=18), ALIGN),
