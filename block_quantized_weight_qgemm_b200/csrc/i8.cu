@@ -22,8 +22,8 @@ namespace qg {
 // Activations: one CTA per row
 // ---------------------------------------------------------------------------------------
 constexpr float kI8Inv = 1.f / 127.f;
-constexpr int kI8QuantThreads = 256;
-constexpr int kI8QuantRegs = 4;  // 8-element words per thread kept in registers (rows to 8192)
+constexpr int kI8QuantThreads = 1024;  // at most
+constexpr int kI8QuantRegs = 4;        // 8-element words per thread kept in registers
 
 struct I8QuantParams {
   const uint16_t* x;  // bf16 [M][K]
@@ -32,37 +32,36 @@ struct I8QuantParams {
   float* scales;  // [M]
 };
 
-// One rounded quotient.  t = x inv + 1.5 2^23 rounds x / s to an integer (in t's low bits) up to
-// the error of inv; r = x - q s then says which side of the half step x lies on.  r is exact:
+// Eight rounded quotients.  t = x inv + 1.5 2^23 rounds x / s to an integer (in t's low bits) up
+// to the error of inv; r = x - q s then says which side of the half step x lies on.  r is exact:
 // where it decides, |x| >= s / 2 makes x and q s multiples of s's last place, and |r| is about
-// s / 2.  So the code is the one of the exact quotient, ties to even.
-__device__ __forceinline__ int i8_code(float x, float inv, float s, float half) {
-  const float magic = 12582912.f;
-  const float t = fmaf(x, inv, magic);
-  const float q = t - magic;
-  const float r = fmaf(-q, s, x);
-  int c = __float_as_int(t);
-  if (fabsf(r) >= half) {
-    const bool odd = c & 1;
-    if (fabsf(r) > half || odd) c += r > 0.f ? 1 : -1;
-  }
-  return c;
-}
-
+// s / 2.  So the code is the one of the exact quotient, ties to even.  A quotient that close to a
+// half step is rare (ties of short significands apart): the words that hold one are corrected in
+// a branch of their own.
+template <bool UP>
 __device__ __forceinline__ uint2 i8_codes8(const uint4& v, float up, float inv, float s, float half) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t o[2];
+  const float magic = 12582912.f;
+  float x[8];
+  int c[8];
+  float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    int c[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      c[2 * h] = i8_code(__uint_as_float(w[2 * i + h] << 16) * up, inv, s, half);
-      c[2 * h + 1] = i8_code(__uint_as_float(w[2 * i + h] & 0xFFFF0000u) * up, inv, s, half);
-    }
-    o[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  for (int i = 0; i < 8; ++i) {
+    x[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
+    if (UP) x[i] *= up;
+    const float t = fmaf(x[i], inv, magic);
+    c[i] = __float_as_int(t);
+    far = fmaxf(far, fabsf(fmaf(-(t - magic), s, x[i])));
   }
-  return make_uint2(o[0], o[1]);
+  if (far >= half) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = fmaf(-(__int_as_float(c[i]) - magic), s, x[i]);
+      if (fabsf(r) > half || (fabsf(r) == half && (c[i] & 1))) c[i] += r > 0.f ? 1 : -1;
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
 // Per row: the largest |x| as bf16 bits (which order like the magnitudes, infinities and NaN
@@ -73,51 +72,54 @@ __global__ void __launch_bounds__(kI8QuantThreads) qgemm_i8_quant_kernel(const I
   griddep_wait();
   griddep_launch_dependents();
   const int64_t m = blockIdx.x;
+  const int step = blockDim.x * 8;
   const uint16_t* xr = p.x + m * p.K;
   __shared__ uint32_t red[kI8QuantThreads / 32];
   uint4 v[kI8QuantRegs];
   uint32_t top = 0;  // two maxima of 16 bits
   auto take = [&](const uint4& a) {
-    top = __vmaxu2(top, a.x & 0x7FFF7FFFu);
-    top = __vmaxu2(top, a.y & 0x7FFF7FFFu);
-    top = __vmaxu2(top, a.z & 0x7FFF7FFFu);
-    top = __vmaxu2(top, a.w & 0x7FFF7FFFu);
+    top = __vmaxu2(top, __vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu));
+    top = __vmaxu2(top, __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
   };
 #pragma unroll
   for (int j = 0; j < kI8QuantRegs; ++j) {
-    const int k = (threadIdx.x + j * kI8QuantThreads) * 8;
+    const int k = threadIdx.x * 8 + j * step;
     v[j] = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0u, 0u, 0u, 0u);
-    take(v[j]);
   }
-  for (int k = (threadIdx.x + kI8QuantRegs * kI8QuantThreads) * 8; k < p.K; k += kI8QuantThreads * 8)
+#pragma unroll
+  for (int j = 0; j < kI8QuantRegs; ++j) take(v[j]);
+  for (int k = threadIdx.x * 8 + kI8QuantRegs * step; k < p.K; k += step)
     take(*reinterpret_cast<const uint4*>(xr + k));
   const uint32_t mx = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
   __syncthreads();
-  uint32_t bits = red[0];
-#pragma unroll
-  for (int i = 1; i < kI8QuantThreads / 32; ++i) bits = max(bits, red[i]);
+  const int lane = threadIdx.x & 31;
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? red[lane] : 0u);
   const bool finite = bits < 0x7F80u;
   const float amax = __uint_as_float(bits << 16);
   const float scale = finite ? __fmul_rn(amax, kI8Inv) : __int_as_float(0x7FC00000);
   if (threadIdx.x == 0) p.scales[m] = scale;
   int8_t* cr = p.codes + m * p.K;
-  if (!finite || bits == 0) {
-    for (int k = threadIdx.x * 8; k < p.K; k += kI8QuantThreads * 8)
-      *reinterpret_cast<uint2*>(cr + k) = make_uint2(0u, 0u);
-    return;
-  }
-  // rows near the bottom of the range are lifted by an exact power of two, scale and all, so that
-  // the reciprocal is finite and the residual normal
-  const float up = amax < 0x1p-60f ? 0x1p64f : 1.f;
-  const float s = scale * up, half = 0.5f * s, inv = __frcp_rn(s);
+  auto write = [&](auto f) {
 #pragma unroll
-  for (int j = 0; j < kI8QuantRegs; ++j) {
-    const int k = (threadIdx.x + j * kI8QuantThreads) * 8;
-    if (k < p.K) *reinterpret_cast<uint2*>(cr + k) = i8_codes8(v[j], up, inv, s, half);
+    for (int j = 0; j < kI8QuantRegs; ++j) {
+      const int k = threadIdx.x * 8 + j * step;
+      if (k < p.K) *reinterpret_cast<uint2*>(cr + k) = f(v[j]);
+    }
+    for (int k = threadIdx.x * 8 + kI8QuantRegs * step; k < p.K; k += step)
+      *reinterpret_cast<uint2*>(cr + k) = f(*reinterpret_cast<const uint4*>(xr + k));
+  };
+  if (!finite || bits == 0) {
+    write([](const uint4&) { return make_uint2(0u, 0u); });
+  } else if (amax >= 0x1p-60f) {
+    const float half = 0.5f * scale, inv = __frcp_rn(scale);
+    write([=](const uint4& a) { return i8_codes8<false>(a, 1.f, inv, scale, half); });
+  } else {
+    // a row near the bottom of the range is lifted by an exact power of two, scale and all, so
+    // that the reciprocal is finite and the residual normal
+    const float up = 0x1p64f, s = scale * up, half = 0.5f * s, inv = __frcp_rn(s);
+    write([=](const uint4& a) { return i8_codes8<true>(a, up, inv, s, half); });
   }
-  for (int k = (threadIdx.x + kI8QuantRegs * kI8QuantThreads) * 8; k < p.K; k += kI8QuantThreads * 8)
-    *reinterpret_cast<uint2*>(cr + k) = i8_codes8(*reinterpret_cast<const uint4*>(xr + k), up, inv, s, half);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -155,9 +157,11 @@ __global__ void __launch_bounds__(256) qgemm_i8_pack_kernel(const float* __restr
 // accumulator sets in tensor memory let the epilogue of a unit run under the MMAs of the next.
 // Warp 0 brings each 128-K chunk into a ring of shared-memory stages (one 16 KB bulk copy per
 // matrix, one or more boxes of x), warp 1 issues four M128 N(rows) K32 MMAs per chunk and matrix,
-// warps 2..5 read the accumulators out.
+// warps 2..9 read the accumulators out.
 // ---------------------------------------------------------------------------------------
-constexpr int kI8Threads = 6 * 32;
+constexpr int kI8EpiWarps = 8;
+constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
+constexpr int kI8Strip = 128;  // row scales per epilogue warp: half of a unit's 256 rows
 constexpr int kI8MaxStages = 12;
 
 __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -262,9 +266,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const uint32_t bar_acc = bar_empty + 8 * kI8MaxStages;  // [2] a unit's accumulators are complete
   const uint32_t bar_acc_free = bar_acc + 16;             // [2] the epilogue has read them
   const uint32_t bar_drain = bar_acc_free + 16;
-  int* ctl = reinterpret_cast<int*>(bars + 2 * kI8MaxStages + 5);
+  int* ctl = reinterpret_cast<int*>(bars + 2 * kI8MaxStages + 6);
   volatile int* abort_flag = ctl + 1;
-  int* pre = ctl + 4;  // routed: [E + 1]
+  float* strip = reinterpret_cast<float*>(ctl + 4);                      // [epilogue warps][kI8Strip]
+  int* pre = reinterpret_cast<int*>(strip + kI8EpiWarps * kI8Strip);     // routed: [E]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0 && lane == 0) {
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_acc + 8 * i, 1);
-      mbar_init(bar_acc_free + 8 * i, 4);
+      mbar_init(bar_acc_free + 8 * i, kI8EpiWarps);
     }
     mbar_init(bar_drain, 1);
     ctl[1] = 0;
@@ -423,52 +428,89 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;
+    // Two warps per lane quarter take alternate 16-row blocks of a unit.  A unit's scales are
+    // loaded while the unit before it is computed and read out: units of few chunks would
+    // otherwise wait for those loads one after another (2048 x 512 experts, 64 tokens top-10 of
+    // 512: see the figures at the launcher).
+    const int q = warp & 3, hw = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    float* sxs = strip + (warp - 2) * kI8Strip;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
-    int i = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-      const I8Unit U = i8_unit(p, pre, u);
+    I8Unit U;
+    float sw[NMAT], sxl[kI8Strip / 32];
+    // strip entry 16 b + r: row r of the warp's b-th block (block 2 b + hw of the unit)
+    auto fetch = [&](int u) {
+      U = i8_unit(p, pre, u);
       const int64_t n = (int64_t)U.t * kTileRows + q * 32 + lane;
-      const bool in = n < p.N;
-      float sw[NMAT];
 #pragma unroll
       for (int m = 0; m < NMAT; ++m) {
         const float* sc = p.off ? p.scales_tab[m][U.ex] : p.scales[m];
-        sw[m] = in ? __ldg(sc + n) : 0.f;
+        sw[m] = n < p.N ? __ldg(sc + n) : 0.f;
       }
+#pragma unroll
+      for (int e = 0; e < kI8Strip / 32; ++e) {
+        const int row = (2 * (2 * e + (lane >> 4)) + hw) * 16 + (lane & 15);
+        sxl[e] = row < U.rows ? p.xscales[U.row0 + row] : 0.f;
+      }
+    };
+    if (blockIdx.x < units) fetch(blockIdx.x);
+    int i = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+      const I8Unit V = U;
+      float swv[NMAT];
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) swv[m] = sw[m];
+#pragma unroll
+      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sxl[e];
+      __syncwarp();
+      const int64_t n = (int64_t)V.t * kTileRows + q * 32 + lane;
+      const bool in = n < p.N;
+      if (u + (int)gridDim.x < units) fetch(u + gridDim.x);
       bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + lane_base + (uint32_t)((i & 1) * set);
-      for (int cb = 0; cb < U.rows; cb += 16) {
+      for (int cb = hw * 16; cb < V.rows; cb += 32) {
+        __syncwarp();
         uint32_t v[NMAT][16];
 #pragma unroll
         for (int m = 0; m < NMAT; ++m) i8_tmem_ld16(d + (uint32_t)(m * p.NB + cb), v[m]);
-        const int nr = min(16, U.rows - cb);
-        const int64_t m0 = U.row0 + cb;
-        const float sxl = (lane < nr) ? p.xscales[m0 + lane] : 0.f;
-        tmem_ld_wait();
+        const float* sxb = sxs + (cb >> 5) * 16;
+        float sx[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float sx = __shfl_sync(0xffffffffu, sxl, r);
-          if (r >= nr || !in) continue;
-          const size_t at = (size_t)(m0 + r) * p.N + n;
-          if (NMAT == 1 && p.S > 1) {
-            p.ws[(size_t)U.s * p.M * p.N + at] = (int)v[0][r];
-            continue;
-          }
-          const float y = __int2float_rn((int)v[0][r]) * sw[0] * sx;
-          if (NMAT == 2)
-            reinterpret_cast<__nv_bfloat16*>(p.out)[at] =
-                __float2bfloat16_rn(silu_mul(y, __int2float_rn((int)v[NMAT - 1][r]) * sw[NMAT - 1] * sx));
-          else if (p.out_bf16)
-            reinterpret_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-          else
-            reinterpret_cast<float*>(p.out)[at] = y;
+        for (int r = 0; r < 16; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(sxb + r);
+          sx[r] = f.x, sx[r + 1] = f.y, sx[r + 2] = f.z, sx[r + 3] = f.w;
         }
+        tmem_ld_wait();
+        const int nr = min(16, V.rows - cb);
+        const size_t at = (size_t)(V.row0 + cb) * p.N + n;
+        if (!in) continue;
+        // 16 rows of one channel: a full block without a branch per row, so that its stores follow
+        // one another
+        auto store = [&](auto* out, auto f) {
+          out += at;
+          if (nr == 16) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) out[(size_t)r * p.N] = f(r);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (r < nr) out[(size_t)r * p.N] = f(r);
+          }
+        };
+        auto y = [&](int m, int r) { return __int2float_rn((int)v[m][r]) * swv[m] * sx[r]; };
+        if (NMAT == 2)
+          store(reinterpret_cast<__nv_bfloat16*>(p.out),
+                [&](int r) { return __float2bfloat16_rn(silu_mul(y(0, r), y(NMAT - 1, r))); });
+        else if (p.S > 1)
+          store(p.ws + (size_t)V.s * p.M * p.N, [&](int r) { return (int)v[0][r]; });
+        else if (p.out_bf16)
+          store(reinterpret_cast<__nv_bfloat16*>(p.out), [&](int r) { return __float2bfloat16_rn(y(0, r)); });
+        else
+          store(reinterpret_cast<float*>(p.out), [&](int r) { return y(0, r); });
       }
       tc_fence_before();
       __syncwarp();
@@ -544,7 +586,10 @@ cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes,
 cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales,
                             cudaStream_t stream) {
   I8QuantParams p{x, (int)K, codes, scales};
-  return launch_dep(qgemm_i8_quant_kernel, dim3((unsigned)M), dim3(kI8QuantThreads), 0, stream, p);
+  // few rows: a thread per word, for the shortest way through a row; many: four words per thread
+  const int64_t words = K / 8, per = M <= 2 * kI8SMs ? 1 : kI8QuantRegs;
+  const int threads = (int)std::min<int64_t>(kI8QuantThreads, ((words + per - 1) / per + 31) / 32 * 32);
+  return launch_dep(qgemm_i8_quant_kernel, dim3((unsigned)M), dim3(threads), 0, stream, p);
 }
 
 
@@ -629,7 +674,8 @@ cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map, cudaStream_t stre
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 5) + 16 + (p.off ? 4 * ((size_t)p.E + 1) : 0) + 64;
+  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 + 4 * kI8EpiWarps * kI8Strip +
+                      (p.off ? 4 * (size_t)p.E : 0);
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
   const int64_t most = (int64_t)p.tiles * p.b_tiles * (p.off ? p.E : p.S);

@@ -7,8 +7,8 @@ missing or fails to load, the call raises -- there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -412,25 +412,38 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
 
 
 # ---- routed tokens: sorted by expert, and back --------------------------------------------
+#
+# These calls take a few microseconds on the device, so the marshalling is kept lean: integer
+# addresses, one pass of checks, sizes remembered per shape.
 
 _ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
 
 
-def _on(*tensors):
-    """The checks every tensor of a routed or int8 call passes: on one CUDA device, contiguous.
-    Returns that device's guard (the library launches on the current device)."""
-    dev = tensors[0].device
+def _at(stream, *tensors):
+    """Checks that the tensors are contiguous on one CUDA device; returns (the device guard a call
+    needs, its stream handle).  The library launches on the current device."""
+    i = tensors[0].get_device()
     for t in tensors:
-        assert t.device == dev and t.is_contiguous()
-    assert dev.type == "cuda"
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NOTHING
+        assert t.get_device() == i >= 0 and t.is_contiguous()
+    here = torch.cuda.current_device()
+    if stream is None:
+        return None if i == here else torch.cuda.device(i), _raw_stream(i)
+    return None if i == here else torch.cuda.device(i), stream.cuda_stream
 
 
-_NOTHING = contextlib.nullcontext()
+def _raw_stream(device_index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device_index)
 
 
-def _nbytes(t) -> int:
-    return t.numel() * t.element_size()
+def _call(name: str, guard, *args):
+    fn = getattr(_lib or lib(), name)
+    if guard is None:
+        status = fn(*args)
+    else:
+        with guard:
+            status = fn(*args)
+    if status != OK:
+        raise QgemmError(status, name)
 
 
 def _scratch(nbytes: int, device, stream):
@@ -441,6 +454,11 @@ def _scratch(nbytes: int, device, stream):
     return t
 
 
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=256)
 def moe_dispatch_workspace_size(T: int, k: int, E: int) -> int:
     b = _SZ()
     _check(lib().qgemm_moe_dispatch_workspace_size(T, k, E, ctypes.byref(b)),
@@ -453,39 +471,44 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
                  workspace=None, stream=None):
     """qgemm_moe_dispatch: tokens x [T, H] (bf16 or fp32) and their experts int32 [T, k] (outside
     [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
-    assert x.dtype in _ROW_DTYPES and x.dim() == 2
-    assert experts.dtype == torch.int32 and experts.dim() == 2 and experts.shape[0] == x.shape[0]
     T, H = x.shape
-    k = experts.shape[1]
+    T2, k = experts.shape
+    dt = _ROW_DTYPES[x.dtype]
+    assert T2 == T and experts.dtype == torch.int32
     if xs is None:
         xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    else:
+        assert xs.dtype == x.dtype and xs.shape == (T * k, H)
     if offsets is None:
         offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+    else:
+        assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
     if rows is None:
         rows = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    assert xs.dtype == x.dtype and xs.shape == (T * k, H)
-    assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
-    assert rows.dtype == torch.int32 and rows.shape == (T, k)
+    else:
+        assert rows.dtype == torch.int32 and rows.shape == (T, k)
     if workspace is None:
         nbytes = moe_dispatch_workspace_size(T, k, E)
-        workspace = _scratch(nbytes, x.device, stream)
-    with _on(x, experts, xs, offsets, rows, workspace):
-        _check(lib().qgemm_moe_dispatch(_ptr(x), _ROW_DTYPES[x.dtype], T, H, _ptr(experts), k, E,
-                                        _ptr(offsets), _ptr(rows), _ptr(xs), _ptr(workspace),
-                                        _nbytes(workspace), _stream(stream)), "qgemm_moe_dispatch")
+        workspace = _scratch(nbytes, x.device, stream) if nbytes else None
+    guard, st = _at(stream, x, experts, xs, offsets, rows, *(() if workspace is None else (workspace,)))
+    _call("qgemm_moe_dispatch", guard, x.data_ptr(), dt, T, H, experts.data_ptr(), k, E, offsets.data_ptr(),
+          rows.data_ptr(), xs.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else _nbytes(workspace), st)
     return xs, offsets, rows
 
 
 def _routed(a, rows):
-    assert a.dtype in _ROW_DTYPES and a.dim() == 2
-    assert rows.dtype == torch.int32 and rows.dim() == 2 and a.shape[0] == rows.numel()
-    return rows.shape[0], rows.shape[1], a.shape[1]
+    """(T, k, H) of sorted rows a [T*k, H] and their map [T, k]."""
+    T, k = rows.shape
+    S, H = a.shape
+    assert S == T * k and rows.dtype == torch.int32
+    return T, k, H
 
 
-def _routed_out(out, shape, dtype, device):
+def _routed_out(out, T, H, dtype, device):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    assert out.dtype in _ROW_DTYPES and out.shape == shape
+        return torch.empty((T, H), dtype=dtype, device=device)
+    assert out.shape == (T, H)
     return out
 
 
@@ -493,11 +516,10 @@ def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | 
                       dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
     T, k, H = _routed(dxs, rows)
-    dx = _routed_out(dx, (T, H), dx_dtype, dxs.device)
-    with _on(dxs, rows, dx):
-        _check(lib().qgemm_moe_dispatch_grad(_ptr(dxs), _ROW_DTYPES[dxs.dtype], T, H, _ptr(rows), k,
-                                             _ptr(dx), _ROW_DTYPES[dx.dtype], _stream(stream)),
-               "qgemm_moe_dispatch_grad")
+    dx = _routed_out(dx, T, H, dx_dtype, dxs.device)
+    guard, st = _at(stream, dxs, rows, dx)
+    _call("qgemm_moe_dispatch_grad", guard, dxs.data_ptr(), _ROW_DTYPES[dxs.dtype], T, H, rows.data_ptr(), k,
+          dx.data_ptr(), _ROW_DTYPES[dx.dtype], st)
     return dx
 
 
@@ -505,12 +527,11 @@ def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
                 y: torch.Tensor | None = None, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_combine: y[t] = sum_j weights[t, j] * ys[rows[t, j]], weights fp32 [T, k]."""
     T, k, H = _routed(ys, rows)
-    assert weights.dtype == torch.float32 and weights.shape == rows.shape
-    y = _routed_out(y, (T, H), y_dtype, ys.device)
-    with _on(ys, rows, weights, y):
-        _check(lib().qgemm_moe_combine(_ptr(ys), _ROW_DTYPES[ys.dtype], T, H, _ptr(rows),
-                                       _ptr(weights), k, _ptr(y), _ROW_DTYPES[y.dtype],
-                                       _stream(stream)), "qgemm_moe_combine")
+    assert weights.dtype == torch.float32 and weights.shape == (T, k)
+    y = _routed_out(y, T, H, y_dtype, ys.device)
+    guard, st = _at(stream, ys, rows, weights, y)
+    _call("qgemm_moe_combine", guard, ys.data_ptr(), _ROW_DTYPES[ys.dtype], T, H, rows.data_ptr(),
+          weights.data_ptr(), k, y.data_ptr(), _ROW_DTYPES[y.dtype], st)
     return y
 
 
@@ -519,18 +540,15 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
     """qgemm_moe_combine_grad: the gradients (dys [T*k, H] in ys's type, dw fp32 [T, k]) of
     moe_combine, given dy [T, H]."""
     T, k, H = _routed(ys, rows)
-    assert weights.dtype == torch.float32 and weights.shape == rows.shape
-    assert dy.dtype in _ROW_DTYPES and dy.shape == (T, H)
-    dys = _routed_out(dys, (T * k, H), ys.dtype, ys.device)
+    assert weights.dtype == torch.float32 and weights.shape == (T, k) and dy.shape == (T, H)
+    dys = _routed_out(dys, T * k, H, ys.dtype, ys.device)
     assert dys.dtype == ys.dtype
-    if dw is None:
-        dw = torch.empty((T, k), dtype=torch.float32, device=ys.device)
-    assert dw.dtype == torch.float32 and dw.shape == rows.shape
-    with _on(dy, ys, rows, weights, dys, dw):
-        _check(lib().qgemm_moe_combine_grad(_ptr(dy), _ROW_DTYPES[dy.dtype], _ptr(ys),
-                                            _ROW_DTYPES[ys.dtype], T, H, _ptr(rows), _ptr(weights),
-                                            k, _ptr(dys), _ptr(dw), _stream(stream)),
-               "qgemm_moe_combine_grad")
+    dw = _routed_out(dw, T, k, torch.float32, ys.device)
+    assert dw.dtype == torch.float32
+    guard, st = _at(stream, dy, ys, rows, weights, dys, dw)
+    _call("qgemm_moe_combine_grad", guard, dy.data_ptr(), _ROW_DTYPES[dy.dtype], ys.data_ptr(),
+          _ROW_DTYPES[ys.dtype], T, H, rows.data_ptr(), weights.data_ptr(), k, dys.data_ptr(),
+          dw.data_ptr(), st)
     return dys, dw
 
 
@@ -559,13 +577,12 @@ class I8Weight:
 
 def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weight:
     """qgemm_i8_pack: W fp32 [N, K] on the device -> I8Weight."""
-    assert W.dtype == torch.float32 and W.dim() == 2
     N, K = W.shape
+    assert W.dtype == torch.float32
     w = out or I8Weight(N, K, W.device)
     assert (w.N, w.K) == (N, K)
-    with _on(W, w.codes, w.scales):
-        _check(lib().qgemm_i8_pack(_ptr(W), N, K, _ptr(w.codes), _ptr(w.scales), _stream(stream)),
-               "qgemm_i8_pack")
+    guard, st = _at(stream, W, w.codes, w.scales)
+    _call("qgemm_i8_pack", guard, W.data_ptr(), N, K, w.codes.data_ptr(), w.scales.data_ptr(), st)
     return w
 
 
@@ -573,56 +590,47 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
                        stream=None) -> I8Weight:
     """qgemm_i8_repack_rowmajor: a checkpoint's int8 codes [N, K] (rows may be strided) and fp32
     scales [N] -> I8Weight.  The scales are kept, not copied."""
-    assert codes_rm.dtype == torch.int8 and codes_rm.dim() == 2 and codes_rm.stride(1) == 1
     N, K = codes_rm.shape
+    assert codes_rm.dtype == torch.int8 and (codes_rm.stride(1) == 1 or K == 1)
     assert scales.dtype == torch.float32 and scales.shape == (N,)
     w = out or I8Weight(N, K, codes_rm.device)
-    assert (w.N, w.K) == (N, K)
+    assert (w.N, w.K) == (N, K) and codes_rm.get_device() == scales.get_device()
     w.scales = scales
-    with _on(w.codes, scales):
-        assert codes_rm.device == scales.device
-        _check(lib().qgemm_i8_repack_rowmajor(N, K, _ptr(codes_rm), codes_rm.stride(0), _ptr(w.codes),
-                                              _stream(stream)), "qgemm_i8_repack_rowmajor")
+    guard, st = _at(stream, w.codes, scales)
+    _call("qgemm_i8_repack_rowmajor", guard, N, K, codes_rm.data_ptr(), codes_rm.stride(0) if N > 1 else K,
+          w.codes.data_ptr(), st)
     return w
 
 
 def i8_quant_x(x: torch.Tensor, stream=None):
     """qgemm_i8_quant_x: x bf16 [M, K] -> (codes int8 [M, K], scales fp32 [M])."""
-    assert x.dtype == torch.bfloat16 and x.dim() == 2
     M, K = x.shape
+    assert x.dtype == torch.bfloat16
     codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
     scales = torch.empty(M, dtype=torch.float32, device=x.device)
-    with _on(x, codes, scales):
-        _check(lib().qgemm_i8_quant_x(_ptr(x), M, K, _ptr(codes), _ptr(scales), _stream(stream)),
-               "qgemm_i8_quant_x")
+    guard, st = _at(stream, x, codes, scales)
+    _call("qgemm_i8_quant_x", guard, x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), st)
     return codes, scales
 
 
+@functools.lru_cache(maxsize=256)
 def i8_workspace_size(N: int, K: int, M: int) -> int:
     b = _SZ()
     _check(lib().qgemm_i8_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_workspace_size")
     return b.value
 
 
-def _i8_y(y, M, N, y_dtype, device):
-    if y is None:
-        y = torch.empty((M, N), dtype=y_dtype, device=device)
-    assert y.dtype in _ROW_DTYPES and y.shape == (M, N)
-    return y
-
-
 def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=torch.float32,
            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """qgemm_i8_run: x bf16 [M, K], quantised per row on the fly -> y [M, N] (fp32 or bf16)."""
-    assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == w.K
     M, K = x.shape
-    y = _i8_y(y, M, w.N, y_dtype, x.device)
+    assert x.dtype == torch.bfloat16 and K == w.K
+    y = _routed_out(y, M, w.N, y_dtype, x.device)
     if workspace is None:
         workspace = _scratch(i8_workspace_size(w.N, K, M), x.device, stream)
-    with _on(x, w.codes, w.scales, y, workspace):
-        _check(lib().qgemm_i8_run(_ptr(x), M, K, _ptr(w.codes), _ptr(w.scales), w.N, _ptr(y),
-                                  _ROW_DTYPES[y.dtype], _ptr(workspace), _nbytes(workspace),
-                                  _stream(stream)), "qgemm_i8_run")
+    guard, st = _at(stream, x, w.codes, w.scales, y, workspace)
+    _call("qgemm_i8_run", guard, x.data_ptr(), M, K, w.codes.data_ptr(), w.scales.data_ptr(), w.N, y.data_ptr(),
+          _ROW_DTYPES[y.dtype], workspace.data_ptr(), _nbytes(workspace), st)
     return y
 
 
@@ -639,41 +647,45 @@ class I8ExpertTable:
         self.experts = experts  # keeps the buffers alive
 
 
+@functools.lru_cache(maxsize=256)
 def i8_moe_workspace_size(N: int, K: int, M: int) -> int:
     b = _SZ()
     _check(lib().qgemm_i8_moe_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_moe_workspace_size")
     return b.value
 
 
+def _i8_moe(x, offsets, tab):
+    M, K = x.shape
+    assert x.dtype == torch.bfloat16 and K == tab.K
+    assert offsets.dtype == torch.int32 and offsets.numel() == tab.E + 1
+    return M, K
+
+
 def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_rows: int,
                y: torch.Tensor | None = None, y_dtype=torch.float32, workspace=None, stream=None):
     """qgemm_i8_moe_run: rows of x grouped by expert (int32 offsets[E+1] on the device)."""
-    _moe_common(x, offsets, tab)
-    M, K = x.shape
-    y = _i8_y(y, M, tab.N, y_dtype, x.device)
+    M, K = _i8_moe(x, offsets, tab)
+    y = _routed_out(y, M, tab.N, y_dtype, x.device)
     if workspace is None:
         workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x.device, stream)
-    with _on(x, offsets, tab.codes, y, workspace):
-        _check(lib().qgemm_i8_moe_run(_ptr(x), M, K, tab.E, _ptr(offsets), max_rows, _ptr(tab.codes),
-                                      _ptr(tab.scales), tab.N, _ptr(y), _ROW_DTYPES[y.dtype],
-                                      _ptr(workspace), _nbytes(workspace), _stream(stream)),
-               "qgemm_i8_moe_run")
+    guard, st = _at(stream, x, offsets, tab.codes, y, workspace)
+    _call("qgemm_i8_moe_run", guard, x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows,
+          tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N, y.data_ptr(), _ROW_DTYPES[y.dtype],
+          workspace.data_ptr(), _nbytes(workspace), st)
     return y
 
 
 def i8_moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: I8ExpertTable, up: I8ExpertTable,
                    max_rows: int, h: torch.Tensor | None = None, workspace=None, stream=None):
     """qgemm_i8_moe_gate_up: h = bf16(SiLU(g) * u) per routed row."""
-    _moe_common(x, offsets, gate)
+    M, K = _i8_moe(x, offsets, gate)
     assert (gate.N, gate.K, gate.E) == (up.N, up.K, up.E)
-    M, K = x.shape
-    h = _i8_y(h, M, gate.N, torch.bfloat16, x.device)
+    h = _routed_out(h, M, gate.N, torch.bfloat16, x.device)
     assert h.dtype == torch.bfloat16
     if workspace is None:
         workspace = _scratch(i8_moe_workspace_size(gate.N, K, M), x.device, stream)
-    with _on(x, offsets, gate.codes, up.codes, h, workspace):
-        _check(lib().qgemm_i8_moe_gate_up(_ptr(x), M, K, gate.E, _ptr(offsets), max_rows,
-                                          _ptr(gate.codes), _ptr(gate.scales), _ptr(up.codes),
-                                          _ptr(up.scales), gate.N, _ptr(h), _ptr(workspace),
-                                          _nbytes(workspace), _stream(stream)), "qgemm_i8_moe_gate_up")
+    guard, st = _at(stream, x, offsets, gate.codes, up.codes, h, workspace)
+    _call("qgemm_i8_moe_gate_up", guard, x.data_ptr(), M, K, gate.E, offsets.data_ptr(), max_rows,
+          gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(),
+          gate.N, h.data_ptr(), workspace.data_ptr(), _nbytes(workspace), st)
     return h
