@@ -375,17 +375,20 @@ bool x_map(CUtensorMap* out, int dev, CUtensorMapDataType dt, const void* base, 
   return true;
 }
 
-// int8 rows: 2-D map {K, rows} of bytes, boxes of 128 x box_rows in the 128-byte swizzle (bytes
-// and rows past the end read zeros).
-bool i8_x_map(CUtensorMap* out, int dev, const void* base, int64_t rows, int64_t K, uint32_t box_rows) {
-  const MapKey k{dev, (int)CU_TENSOR_MAP_DATA_TYPE_UINT8, 0, base, rows, K, K, box_rows, 1};
+// int8 codes: 2-D map {row_bytes, rows} of contiguous rows, boxes of 128 bytes x box_rows, in the
+// 128-byte swizzle or, for codes already stored in it, as they are (bytes and rows past the end
+// read zeros).
+bool i8_map(CUtensorMap* out, int dev, const void* base, int64_t rows, int64_t row_bytes, uint32_t box_rows,
+            bool swizzle) {
+  const MapKey k{dev, (int)CU_TENSOR_MAP_DATA_TYPE_UINT8, 0, base, rows, row_bytes, row_bytes, box_rows,
+                 swizzle ? 1u : 0u};
   for (int i = 0; i < g_maps.used; ++i)
     if (g_maps.key[i] == k) {
       *out = g_maps.map[i];
       return true;
     }
-  if (!make_map(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, (uint64_t)K, (uint64_t)rows, (uint64_t)K, 128,
-                box_rows, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!make_map(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, (uint64_t)row_bytes, (uint64_t)rows,
+                (uint64_t)row_bytes, 128, box_rows, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
     return false;
   const int i = g_maps.next;
   g_maps.key[i] = k;
@@ -1227,14 +1230,18 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   i8_plan(N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, routed, &p);
+  if (!routed && p.units == 0) return QGEMM_ERR_SHAPE;  // more than 2^30 units
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
   p.xcodes = reinterpret_cast<const int8_t*>(wsb);
   p.xscales = reinterpret_cast<const float*>(wsb + w.scales);
   p.ws = reinterpret_cast<int*>(wsb + w.partials);
-  CUtensorMap map;
-  if (!i8_x_map(&map, dev, wsb, M, K, (uint32_t)p.box)) {
+  CUtensorMap map, map_w{};
+  const int64_t w_rows = row_tiles(N) * p.chunks * kTileRows;  // the codes as rows of 128 bytes
+  if (p.pair && w_rows > 0x7FFFFFFF - 512 * (int64_t)p.chunks) return QGEMM_ERR_SHAPE;
+  if (!i8_map(&map, dev, wsb, M, K, (uint32_t)p.box, true) ||
+      (p.pair && !i8_map(&map_w, dev, p.codes[0], w_rows, 128, 128, false))) {
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled failed");
     return QGEMM_ERR_CUDA;
   }
@@ -1242,7 +1249,7 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
                                   reinterpret_cast<float*>(wsb + w.scales), s);
   if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
   if (g_prof_begin) cudaEventRecord(g_prof_begin, s);
-  e = launch_i8_gemm(p, map, s);
+  e = launch_i8_gemm(p, map, map_w, s);
   if (e != cudaSuccess) return cuda_fail(e, "int8 gemm launch");
   if (g_prof_end) cudaEventRecord(g_prof_end, s);
   return QGEMM_OK;

@@ -163,6 +163,7 @@ constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
 constexpr int kI8Strip = 128;  // row scales per epilogue warp: half of a unit's 256 rows
 constexpr int kI8MaxStages = 12;
+constexpr int kI8List = 128;  // units of a CTA found ahead (routed)
 
 __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -173,9 +174,9 @@ __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t adesc, uint64_t bdes
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::i8: D s32 (2), A and B signed 8-bit (1), M = 128, N = n.
-__device__ __forceinline__ uint32_t i8_idesc(int n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// Instruction descriptor, kind::i8: D s32 (2), A and B signed 8-bit (1).
+__device__ __forceinline__ uint32_t i8_idesc(int m, int n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 __device__ __forceinline__ void i8_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -209,8 +210,13 @@ __device__ __forceinline__ void i8_load_x(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// One unit of work: rows row0 .. row0+rows-1 of x, a 128-channel tile (for a CTA pair: its two), chunks
+// c0 .. c1-1, and the buffers of each matrix.  part >= 0: the int32 partial it writes.
+template <int NMAT>
 struct I8Unit {
-  int ex, t, row0, rows, c0, c1, s;  // rows row0 .. row0+rows-1 of x, chunks c0 .. c1-1
+  int t, row0, rows, c0, c1, part;
+  const uint8_t* w[NMAT];  // the matrix's codes
+  const float* sc[NMAT];   // its channel scales
 };
 
 // Rows of expert ex: its first row and how many of them are computed.
@@ -219,10 +225,14 @@ __device__ __forceinline__ int i8_expert_rows(const I8Params& p, int ex, int& lo
   return min(min(max(__ldg(p.off + ex + 1), lo), p.M) - lo, p.max_rows);
 }
 
-// Unit u.  Routed: pre[e] is the number of units before expert e's.
-__device__ __forceinline__ I8Unit i8_unit(const I8Params& p, const int* pre, int u) {
-  I8Unit U;
-  int bt;
+// Unit u.  Routed: pre[e] is the number of units before expert e's.  Plain: the first `full` units
+// take all of K, the tiles after them are split in S ranges each.
+template <int NMAT>
+__device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pre, int u) {
+  I8Unit<NMAT> U;
+  U.c0 = 0;
+  U.c1 = p.chunks;
+  U.part = -1;
   if (p.off) {
     int a = 0, b = p.E;  // the last e with pre[e] <= u
     while (b - a > 1) {
@@ -230,27 +240,104 @@ __device__ __forceinline__ I8Unit i8_unit(const I8Params& p, const int* pre, int
       if (pre[m] <= u) a = m;
       else b = m;
     }
-    U.ex = a;
     int lo;
     const int n = i8_expert_rows(p, a, lo);
     const int r = u - pre[a], bts = (n + p.NB - 1) / p.NB;
-    bt = r % bts;
+    const int bt = r % bts;
     U.t = r / bts;
     U.row0 = lo + bt * p.NB;
     U.rows = min(p.NB, n - bt * p.NB);
-    U.s = 0;
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      U.w[m] = p.codes_tab[m][a];
+      U.sc[m] = p.scales_tab[m][a];
+    }
   } else {
-    U.ex = 0;
-    bt = u % p.b_tiles;
-    u /= p.b_tiles;
-    U.s = u % p.S;
-    U.t = u / p.S;
+    if (u >= p.full) {
+      const int r = u - p.full, s = r % p.S;
+      U.part = r;
+      U.c0 = (int)((int64_t)s * p.chunks / p.S);
+      U.c1 = (int)((int64_t)(s + 1) * p.chunks / p.S);
+      u = p.full + r / p.S;
+    }
+    const int bt = u % p.b_tiles;
+    U.t = u / p.b_tiles;
     U.row0 = bt * p.NB;
     U.rows = min(p.NB, p.M - bt * p.NB);
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      U.w[m] = p.codes[m];
+      U.sc[m] = p.scales[m];
+    }
   }
-  U.c0 = (int)((int64_t)U.s * p.chunks / p.S);
-  U.c1 = (int)((int64_t)(U.s + 1) * p.chunks / p.S);
   return U;
+}
+
+// The scales of one epilogue warp's part of a unit: its lane's channel n, and the rows of its
+// 16-row blocks (block b of the warp is block 2 b + hw of the unit; entry 16 b + r is its row r).
+template <int NMAT>
+struct I8Scales {
+  float sw[NMAT], sx[kI8Strip / 32];
+  __device__ __forceinline__ void fetch(const I8Params& p, const I8Unit<NMAT>& U, int64_t n, int hw, int lane) {
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) sw[m] = n < p.N ? __ldg(U.sc[m] + n) : 0.f;
+#pragma unroll
+    for (int e = 0; e < kI8Strip / 32; ++e) {
+      const int row = (2 * (2 * e + (lane >> 4)) + hw) * 16 + (lane & 15);
+      sx[e] = row < U.rows ? p.xscales[U.row0 + row] : 0.f;
+    }
+  }
+};
+
+// The read-out of one warp's part of a unit's accumulators (d: its lane quarter's first column).
+// ch: the lane's channel within the unit, of `width`.
+template <int NMAT>
+__device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT>& V, uint32_t d, int hw, int64_t n,
+                                            int ch, int width, const float (&sw)[NMAT], const float* sxs) {
+  const bool in = n < p.N;
+  for (int cb = hw * 16; cb < V.rows; cb += 32) {
+    __syncwarp();
+    uint32_t v[NMAT][16];
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) i8_tmem_ld16(d + (uint32_t)(m * p.NB + cb), v[m]);
+    const float* sxb = sxs + (cb >> 5) * 16;
+    float sx[16];
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(sxb + r);
+      sx[r] = f.x, sx[r + 1] = f.y, sx[r + 2] = f.z, sx[r + 3] = f.w;
+    }
+    tmem_ld_wait();
+    const int nr = min(16, V.rows - cb);
+    // 16 rows of one channel: a full block without a branch per row, so that its stores follow one
+    // another
+    auto store = [&](auto* out, size_t pitch, auto f) {
+      if (nr == 16) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) out[(size_t)r * pitch] = f(r);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (r < nr) out[(size_t)r * pitch] = f(r);
+      }
+    };
+    auto y = [&](int m, int r) { return __int2float_rn((int)v[m][r]) * sw[m] * sx[r]; };
+    const size_t at = (size_t)(V.row0 + cb) * p.N + n;
+    if (!in) continue;
+    if (NMAT == 2)
+      store(reinterpret_cast<__nv_bfloat16*>(p.out) + at, p.N,
+            [&](int r) { return __float2bfloat16_rn(silu_mul(y(0, r), y(NMAT - 1, r))); });
+    else if (V.part >= 0)
+      store(p.ws + ((size_t)V.part * p.NB + cb) * width + ch, width, [&](int r) { return (int)v[0][r]; });
+    else if (p.out_bf16)
+      store(reinterpret_cast<__nv_bfloat16*>(p.out) + at, p.N, [&](int r) { return __float2bfloat16_rn(y(0, r)); });
+    else
+      store(reinterpret_cast<float*>(p.out) + at, p.N, [&](int r) { return y(0, r); });
+  }
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* a) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
 }
 
 template <int NMAT>
@@ -268,8 +355,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const uint32_t bar_drain = bar_acc_free + 16;
   int* ctl = reinterpret_cast<int*>(bars + 2 * kI8MaxStages + 6);
   volatile int* abort_flag = ctl + 1;
-  float* strip = reinterpret_cast<float*>(ctl + 4);                      // [epilogue warps][kI8Strip]
-  int* pre = reinterpret_cast<int*>(strip + kI8EpiWarps * kI8Strip);     // routed: [E]
+  float* strip = reinterpret_cast<float*>(ctl + 4);  // [epilogue warps][kI8Strip]
+  // routed: the CTA's first units, then [E] the units before each expert's
+  I8Unit<NMAT>* list = reinterpret_cast<I8Unit<NMAT>*>(strip + kI8EpiWarps * kI8Strip);
+  int* pre = reinterpret_cast<int*>(list + kI8List);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0 && lane == 0) {
@@ -326,12 +415,19 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       units += red[i];
     }
     for (int e = e0; e < e1; ++e) pre[e] += base;
+    __syncthreads();
+    // every thread finds one unit of this CTA, so that the roles below read it in one step
+    for (int i = threadIdx.x; i < kI8List; i += kI8Threads) {
+      const int64_t u = (int64_t)blockIdx.x + (int64_t)i * gridDim.x;
+      if (u < units) list[i] = i8_unit<NMAT>(p, pre, (int)u);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
   const int set = NMAT * p.NB;  // columns of one accumulator set
+  auto unit = [&](int i, int u) { return p.off && i < kI8List ? list[i] : i8_unit<NMAT>(p, pre, u); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -339,14 +435,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       const uint64_t pol_w = p.w_again ? policy_evict_last() : policy_evict_first();
       const uint64_t pol_x = policy_evict_last();
       RingPos sp;
-      int issued = 0;
+      int issued = 0, i = 0;
       bool ok = true, waited = false;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        const I8Unit U = i8_unit(p, pre, u);
-        const uint8_t* w[NMAT];
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m)
-          w[m] = (p.off ? p.codes_tab[m][U.ex] : p.codes[m]) + (int64_t)U.t * p.chunks * kWCodeBytes;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
+        const I8Unit<NMAT> U = unit(i, u);
+        const int64_t n0 = (int64_t)U.t * kTileRows;
         const int boxes = (U.rows + p.box - 1) / p.box;
         const uint32_t bytes = (uint32_t)(NMAT * kWCodeBytes + boxes * p.box * 128);
         for (int c = U.c0; c < U.c1; ++c) {
@@ -360,7 +453,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
           for (int m = 0; m < NMAT; ++m)
-            bulk_load(st + m * kWCodeBytes, w[m] + (int64_t)c * kWCodeBytes, kWCodeBytes, fb, pol_w);
+            bulk_load(st + m * kWCodeBytes, U.w[m] + ((int64_t)U.t * p.chunks + c) * kWCodeBytes, kWCodeBytes, fb,
+                      pol_w);
+          if (c == U.c0)
+            // the unit's channel scales, into L2 ahead of the epilogue
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m)
+              for (int64_t n = n0; n < n0 + kTileRows && n < p.N; n += 32) prefetch_l2(U.sc[m] + n);
           if (!waited) {
             griddep_wait();  // the codes of x come from the preceding grid
             waited = true;
@@ -386,8 +485,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       bool ok = true;
       int i = 0;
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
-        const I8Unit U = i8_unit(p, pre, u);
-        const uint32_t idesc = i8_idesc((U.rows + 15) & ~15);
+        const I8Unit<NMAT> U = unit(i, u);
+        const uint32_t idesc = i8_idesc(128, (U.rows + 15) & ~15);
         const uint32_t d = tmem + (uint32_t)((i & 1) * set);
         if (i >= 2) {
           if (!mbar_wait_spin(bar_acc_free + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, false, abort_flag,
@@ -429,89 +528,35 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   } else {
     // ------------------------------------------------------------ epilogue
     // Two warps per lane quarter take alternate 16-row blocks of a unit.  A unit's scales are
-    // loaded while the unit before it is computed and read out: units of few chunks would
-    // otherwise wait for those loads one after another (2048 x 512 experts, 64 tokens top-10 of
-    // 512: see the figures at the launcher).
-    const int q = warp & 3, hw = (warp - 2) >> 2;
+    // loaded while the unit before it is computed and read out.
+    const int q = warp & 3, hw = (warp - 2) >> 2, ch = q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     float* sxs = strip + (warp - 2) * kI8Strip;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
-    I8Unit U;
-    float sw[NMAT], sxl[kI8Strip / 32];
-    // strip entry 16 b + r: row r of the warp's b-th block (block 2 b + hw of the unit)
-    auto fetch = [&](int u) {
-      U = i8_unit(p, pre, u);
-      const int64_t n = (int64_t)U.t * kTileRows + q * 32 + lane;
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m) {
-        const float* sc = p.off ? p.scales_tab[m][U.ex] : p.scales[m];
-        sw[m] = n < p.N ? __ldg(sc + n) : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < kI8Strip / 32; ++e) {
-        const int row = (2 * (2 * e + (lane >> 4)) + hw) * 16 + (lane & 15);
-        sxl[e] = row < U.rows ? p.xscales[U.row0 + row] : 0.f;
-      }
+    I8Unit<NMAT> U;
+    I8Scales<NMAT> sc;
+    auto fetch = [&](int i, int u) {
+      U = unit(i, u);
+      sc.fetch(p, U, (int64_t)U.t * kTileRows + ch, hw, lane);
     };
-    if (blockIdx.x < units) fetch(blockIdx.x);
+    if (blockIdx.x < units) fetch(0, blockIdx.x);
     int i = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-      const I8Unit V = U;
-      float swv[NMAT];
+      const I8Unit<NMAT> V = U;
+      float sw[NMAT];
 #pragma unroll
-      for (int m = 0; m < NMAT; ++m) swv[m] = sw[m];
+      for (int m = 0; m < NMAT; ++m) sw[m] = sc.sw[m];
 #pragma unroll
-      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sxl[e];
+      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sc.sx[e];
       __syncwarp();
-      const int64_t n = (int64_t)V.t * kTileRows + q * 32 + lane;
-      const bool in = n < p.N;
-      if (u + (int)gridDim.x < units) fetch(u + gridDim.x);
+      if (u + (int)gridDim.x < units) fetch(i + 1, u + gridDim.x);
       bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + lane_base + (uint32_t)((i & 1) * set);
-      for (int cb = hw * 16; cb < V.rows; cb += 32) {
-        __syncwarp();
-        uint32_t v[NMAT][16];
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m) i8_tmem_ld16(d + (uint32_t)(m * p.NB + cb), v[m]);
-        const float* sxb = sxs + (cb >> 5) * 16;
-        float sx[16];
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(sxb + r);
-          sx[r] = f.x, sx[r + 1] = f.y, sx[r + 2] = f.z, sx[r + 3] = f.w;
-        }
-        tmem_ld_wait();
-        const int nr = min(16, V.rows - cb);
-        const size_t at = (size_t)(V.row0 + cb) * p.N + n;
-        if (!in) continue;
-        // 16 rows of one channel: a full block without a branch per row, so that its stores follow
-        // one another
-        auto store = [&](auto* out, auto f) {
-          out += at;
-          if (nr == 16) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) out[(size_t)r * p.N] = f(r);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (r < nr) out[(size_t)r * p.N] = f(r);
-          }
-        };
-        auto y = [&](int m, int r) { return __int2float_rn((int)v[m][r]) * swv[m] * sx[r]; };
-        if (NMAT == 2)
-          store(reinterpret_cast<__nv_bfloat16*>(p.out),
-                [&](int r) { return __float2bfloat16_rn(silu_mul(y(0, r), y(NMAT - 1, r))); });
-        else if (p.S > 1)
-          store(p.ws + (size_t)V.s * p.M * p.N, [&](int r) { return (int)v[0][r]; });
-        else if (p.out_bf16)
-          store(reinterpret_cast<__nv_bfloat16*>(p.out), [&](int r) { return __float2bfloat16_rn(y(0, r)); });
-        else
-          store(reinterpret_cast<float*>(p.out), [&](int r) { return y(0, r); });
-      }
+      i8_read_out<NMAT>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw, (int64_t)V.t * kTileRows + ch, ch,
+                        kTileRows, sw, sxs);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
@@ -527,32 +572,231 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   }
 }
 
-// Sum of the K ranges' partials (integers: any order gives the same bits), scales, output.
+// ---------------------------------------------------------------------------------------
+// Wide plain calls (more than 256 rows): the same roles on CTA pairs.  A tile is 256 channels (128 in
+// each CTA's tensor memory) x 256 rows; each CTA loads its own 128 channels and half of the rows,
+// 32 KB per 128-K chunk where a lone CTA's 128 x 256 tile takes 48 KB for the same MMA time.  All
+// loads of a stage count on the even CTA's barrier (the tile-major codes by a tensor map too), so no
+// thread stands between the copies and the MMAs.
+// ---------------------------------------------------------------------------------------
+constexpr int kI8PairStage = 2 * kWCodeBytes;
+constexpr int kI8PairStages = 6;
+
+__device__ __forceinline__ void i8_mma_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
+    qgemm_i8_pair_kernel(const __grid_constant__ I8Params p, const __grid_constant__ CUtensorMap tm_x,
+                         const __grid_constant__ CUtensorMap tm_w) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  constexpr int NST = kI8PairStages;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NST * kI8PairStage);
+  const uint32_t bar_full = smem_u32(bars);       // (even CTA) both CTAs' loads of the stage
+  const uint32_t bar_empty = bar_full + 8 * NST;  // the stage's MMAs are done
+  const uint32_t bar_acc = bar_empty + 8 * NST;   // [2] a tile's accumulators are complete
+  const uint32_t bar_acc_free = bar_acc + 16;     // [2] (even CTA) both epilogues have read them
+  const uint32_t bar_drain = bar_acc_free + 16;
+  int* ctl = reinterpret_cast<int*>(bars + 2 * NST + 6);
+  volatile int* abort_flag = ctl + 1;
+  float* strip = reinterpret_cast<float*>(ctl + 4);  // [epilogue warps][kI8Strip]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_acc + 8 * i, 1);
+      mbar_init(bar_acc_free + 8 * i, 2 * kI8EpiWarps);
+    }
+    mbar_init(bar_drain, 1);
+    ctl[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(ctl), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are initialised before any load or commit counts on them
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (of this CTA's half)
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      const uint32_t full0 = mapa_shared(bar_full, 0);
+      RingPos sp;
+      int issued = 0;
+      bool ok = true, waited = false;
+      for (int u = pid; u < p.units && ok; u += pairs) {
+        const I8Unit<1> U = i8_unit<1>(p, nullptr, u);
+        const int64_t t = 2 * (int64_t)U.t + rank;
+        const int half = ((U.rows + 31) & ~31) >> 1;  // rows of the MMA's N that each CTA holds
+        for (int c = U.c0; c < U.c1; ++c) {
+          if (issued >= NST &&
+              !mbar_wait(bar_empty + 8 * sp.slot, sp.phase ^ 1u, abort_flag, p.dev_err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = sbase + (uint32_t)(sp.slot * kI8PairStage);
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * sp.slot, 2 * kI8PairStage);
+          // (a tile past the matrix reads zeros)
+          tma_load_2d_pair(st, &tm_w, full0 + 8u * sp.slot, 0, (int)((t * p.chunks + c) * kTileRows), pol);
+          if (!waited) {
+            griddep_wait();  // the codes of x come from the preceding grid
+            waited = true;
+          }
+          tma_load_2d_pair(st + kWCodeBytes, &tm_x, full0 + 8u * sp.slot, c * 128, U.row0 + (int)rank * half, pol);
+          sp.next(NST);
+          ++issued;
+        }
+      }
+      if (!ok) {
+        // the copies in flight count on the even CTA's barrier: give them a fixed grace period
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (rank == 0 && lane == 0) {
+      RingPos sp;
+      bool ok = true;
+      int i = 0;
+      for (int u = pid; u < p.units && ok; u += pairs, ++i) {
+        const I8Unit<1> U = i8_unit<1>(p, nullptr, u);
+        const uint32_t idesc = i8_idesc(256, (U.rows + 31) & ~31);
+        const uint32_t d = tmem + (uint32_t)((i & 1) * 256);
+        if (i >= 2) {
+          if (!mbar_wait_spin(bar_acc_free + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, true, abort_flag,
+                              p.dev_err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        for (int c = U.c0; c < U.c1; ++c) {
+          if (!mbar_wait_spin(bar_full + 8 * sp.slot, sp.phase, true, abort_flag, p.dev_err, kErrTimeout)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = sbase + (uint32_t)(sp.slot * kI8PairStage);
+          const uint64_t ad = smem_desc_sw128(st), bd = smem_desc_sw128(st + kWCodeBytes);
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb)
+            i8_mma_pair(d, ad + (uint64_t)(kb * 2), bd + (uint64_t)(kb * 2), idesc, (c != U.c0 || kb != 0) ? 1u : 0u);
+          mma_commit_pair(bar_empty + 8 * sp.slot);
+          sp.next(NST);
+        }
+        if (!ok) break;
+        mma_commit_pair(bar_acc + 8 * (i & 1));
+      }
+      mma_commit_pair(bar_drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar_drain, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue (of this CTA's channels)
+    const int q = warp & 3, hw = (warp - 2) >> 2, ch = (int)rank * kTileRows + q * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    float* sxs = strip + (warp - 2) * kI8Strip;
+    const uint32_t free0 = mapa_shared(bar_acc_free, 0);
+    griddep_wait();  // the scales of x come from the preceding grid
+    griddep_launch_dependents();
+    I8Unit<1> U;
+    I8Scales<1> sc;
+    auto fetch = [&](int u) {
+      U = i8_unit<1>(p, nullptr, u);
+      sc.fetch(p, U, (int64_t)U.t * 2 * kTileRows + ch, hw, lane);
+    };
+    if (pid < p.units) fetch(pid);
+    int i = 0;
+    for (int u = pid; u < p.units; u += pairs, ++i) {
+      const I8Unit<1> V = U;
+      const float sw[1] = {sc.sw[0]};
+#pragma unroll
+      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sc.sx[e];
+      __syncwarp();
+      if (u + pairs < p.units) fetch(u + pairs);
+      bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      i8_read_out<1>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
+                     2 * kTileRows, sw, sxs);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
+        else mbar_arrive_cluster_relaxed(free0 + 8u * (uint32_t)(i & 1));
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  // neither CTA leaves, or frees tensor memory the pair's MMAs write, while its peer may use it
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Sum of the K ranges' partials of the split tiles (integers: any order gives the same bits),
+// scales, output.  One block per 8 rows of a split tile.
+constexpr int kI8ReduceRows = 8;
 __global__ void __launch_bounds__(256) qgemm_i8_reduce_kernel(const I8Params p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t MN = (int64_t)p.M * p.N;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= MN) return;
-  const int lim = (int)min((int64_t)4, MN - at);
-  int acc[4] = {0, 0, 0, 0};
-  const bool vec = (MN & 3) == 0;
-  for (int s = 0; s < p.S; ++s) {
-    const int* src = p.ws + s * MN + at;
-    if (vec) {
-      const int4 v = __ldcs(reinterpret_cast<const int4*>(src));
-      acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
-    } else {
-      for (int e = 0; e < lim; ++e) acc[e] += __ldcs(src + e);
+  const int width = p.pair ? 2 * kTileRows : kTileRows;
+  const int u = p.full + blockIdx.x;  // the tile
+  const int row0 = u % p.b_tiles * p.NB, rows = min(p.NB, p.M - row0);
+  const int64_t n0 = (int64_t)(u / p.b_tiles) * width;
+  const int quads = width / 4;  // threads along a row
+  const int64_t n = n0 + threadIdx.x % quads * 4;
+  for (int r = blockIdx.y * kI8ReduceRows + threadIdx.x / quads; r < min(rows, (int)(blockIdx.y + 1) * kI8ReduceRows);
+       r += 256 / quads) {
+    const int* src = p.ws + (size_t)blockIdx.x * p.S * p.NB * width + (size_t)r * width + threadIdx.x % quads * 4;
+    int4 a = make_int4(0, 0, 0, 0);
+    for (int s = 0; s < p.S; ++s) {
+      const int4 v = __ldcs(reinterpret_cast<const int4*>(src + (size_t)s * p.NB * width));
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
-  }
-  for (int e = 0; e < lim; ++e) {
-    const int64_t m = (at + e) / p.N, n = (at + e) % p.N;
-    const float y = __int2float_rn(acc[e]) * p.scales[0][n] * p.xscales[m];
-    if (p.out_bf16)
-      reinterpret_cast<__nv_bfloat16*>(p.out)[at + e] = __float2bfloat16_rn(y);
-    else
-      reinterpret_cast<float*>(p.out)[at + e] = y;
+    const int acc[4] = {a.x, a.y, a.z, a.w};
+    const float sx = p.xscales[row0 + r];
+    const size_t at = (size_t)(row0 + r) * p.N + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= p.N) break;
+      const float y = __int2float_rn(acc[e]) * p.scales[0][n + e] * sx;
+      if (p.out_bf16)
+        reinterpret_cast<__nv_bfloat16*>(p.out)[at + e] = __float2bfloat16_rn(y);
+      else
+        reinterpret_cast<float*>(p.out)[at + e] = y;
+    }
   }
 }
 
@@ -603,35 +847,35 @@ static int sm_count(int dev) {
   return v;
 }
 
-// K ranges of a plain product: the smallest S of least cost, in units of the time one SM takes to
-// stream a 16 KB chunk at its share of the memory (0.37 us): rounds of units, each its chunks and
-// about four more to start and end; the partials' way out and back through L2 (8 bytes per
-// element at about 5 TB/s); and the reduction's launch (about eight).
-static int i8_split(int64_t T, int64_t b_tiles, int64_t C, int64_t MN) {
-  int best = 1;
-  double best_cost = 0.0;
-  for (int64_t S = 1; S <= std::min<int64_t>(32, C); ++S) {
-    const double rounds = double((T * b_tiles * S + kI8SMs - 1) / kI8SMs);
-    const double cost = rounds * (double((C + S - 1) / S) + 4.0) +
-                        (S > 1 ? 8.0 + double(S) * double(MN) * 8.0 / 5e6 / 0.37 : 0.0);
-    if (S == 1 || cost < best_cost - 1e-9) {
-      best_cost = cost;
-      best = (int)S;
-    }
-  }
-  return best;
-}
-
 // Tiling of a call: rows is M, or the most rows an expert has.
+//
+// A plain call's tiles go out in full rounds over the SMs (or pairs), each tile over all of K; the tiles
+// of the last round, if they leave SMs idle, are split over K so that their ranges fill it.  A split
+// costs the partials' way through L2 and the reduction's launch, about the time of kI8SplitChunks
+// chunks, so it has to save more than those.
+constexpr int kI8SplitChunks = 8;
+
 void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params* p) {
-  p->tiles = (int)row_tiles(N);
+  p->pair = !routed && rows > 256;
+  p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
   p->chunks = (int)k_chunks(FMT_FP8, K);
   const int cap = nmat == 2 ? 128 : 256;
   p->NB = (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16);
   // routed: small boxes, so that an expert's rows bring few of its neighbours' with them
-  p->box = routed ? std::min(p->NB, 32) : p->NB;
+  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, 32) : p->NB;
   p->b_tiles = (int)((rows + p->NB - 1) / p->NB);
-  p->S = routed ? 1 : i8_split(p->tiles, p->b_tiles, p->chunks, rows * N);
+  p->S = 1;
+  p->full = p->units = 0;
+  if (!routed) {
+    const int64_t all = (int64_t)p->tiles * p->b_tiles, slots = p->pair ? kI8SMs / 2 : kI8SMs;
+    const int64_t rest = all % slots;
+    const int64_t S = rest ? std::min<int64_t>(slots / rest, p->chunks) : 1;
+    if (S > 1 && p->chunks - (p->chunks + S - 1) / S > kI8SplitChunks) p->S = (int)S;
+    if (all <= 0x3FFFFFFF) {
+      p->full = (int)(p->S > 1 ? all - rest : all);
+      p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
+    }
+  }
   p->w_again = p->b_tiles > 1;
   p->stage_bytes = nmat * kWCodeBytes + (p->NB + p->box - 1) / p->box * p->box * 128;
   int cols = 32;
@@ -642,20 +886,20 @@ void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params
 size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M) {
   I8Params p{};
   i8_plan(N, K, M, 1, false, &p);
-  return p.S > 1 ? (size_t)p.S * (size_t)M * (size_t)N * 4 : 0;
+  return (size_t)(p.units - p.full) * (size_t)p.NB * (p.pair ? 2 : 1) * kTileRows * 4;
 }
 
-template <int NMAT>
-static cudaError_t launch_i8_impl(const I8Params& p, size_t smem, int grid, const CUtensorMap& map, int dev,
-                                  cudaStream_t stream) {
-  auto kern = qgemm_i8_kernel<NMAT>;
-  static std::atomic<uint64_t> set_mask{0};
+// Raises a kernel's dynamic shared-memory limit once per device (devices beyond 64: every time).
+static cudaError_t raise_smem(const void* kern, std::atomic<uint64_t>& set_mask, int dev) {
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
-  if (bit == 0 || !(set_mask.load(std::memory_order_acquire) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 64);
-    if (e != cudaSuccess) return e;
-    set_mask.fetch_or(bit, std::memory_order_release);
-  }
+  if (bit != 0 && (set_mask.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 64);
+  if (e == cudaSuccess) set_mask.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <typename... P, typename... A>
+static cudaError_t launch_gemm(void (*kern)(P...), size_t smem, int grid, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kI8Threads, 1, 1);
@@ -666,28 +910,45 @@ static cudaError_t launch_i8_impl(const I8Params& p, size_t smem, int grid, cons
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, map);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// p: planned (i8_plan), operands filled in; map: x's codes in boxes of 128 x p.box.
-cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map, cudaStream_t stream) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+template <int NMAT>
+static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> set_mask{0};
+  const cudaError_t e = raise_smem((const void*)qgemm_i8_kernel<NMAT>, set_mask, dev);
   if (e != cudaSuccess) return e;
   const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 + 4 * kI8EpiWarps * kI8Strip +
-                      (p.off ? 4 * (size_t)p.E : 0);
+                      (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : 0);
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
-  const int64_t most = (int64_t)p.tiles * p.b_tiles * (p.off ? p.E : p.S);
-  if (most > 0x3FFFFFFF) return cudaErrorInvalidValue;
-  p.units = (int)most;  // routed: the kernel counts the units that have rows
+  // routed: an upper bound, the kernel counts the units that have rows
+  const int64_t most = p.off ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M) : p.units;
   const int grid = (int)std::min<int64_t>(most, sm_count(dev));
-  const size_t smem = misc + (size_t)p.stages * p.stage_bytes;
-  const cudaError_t g = p.nmat == 2 ? launch_i8_impl<2>(p, smem, grid, map, dev, stream)
-                                    : launch_i8_impl<1>(p, smem, grid, map, dev, stream);
-  if (g != cudaSuccess || p.S == 1) return g;
-  const int64_t quads = ((int64_t)p.M * p.N + 3) / 4;
-  return launch_dep(qgemm_i8_reduce_kernel, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, p);
+  return launch_gemm(qgemm_i8_kernel<NMAT>, misc + (size_t)p.stages * p.stage_bytes, grid, stream, p, map);
+}
+
+// p: planned (i8_plan), operands filled in; map_x: x's codes in boxes of 128 x p.box; map_w (pair):
+// the packed codes in boxes of 128 x 128.
+cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorMap& map_w, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (p.pair) {
+    static std::atomic<uint64_t> set_mask{0};
+    e = raise_smem((const void*)qgemm_i8_pair_kernel, set_mask, dev);
+    if (e != cudaSuccess) return e;
+    const size_t smem = 1024 + kI8PairStages * kI8PairStage + 8 * (2 * kI8PairStages + 6) + 16 +
+                        4 * kI8EpiWarps * kI8Strip;
+    const int grid = 2 * std::min(p.units, sm_count(dev) / 2);
+    e = launch_gemm(qgemm_i8_pair_kernel, smem, grid, stream, p, map_x, map_w);
+  } else {
+    e = p.nmat == 2 ? launch_i8_impl<2>(p, map_x, dev, stream) : launch_i8_impl<1>(p, map_x, dev, stream);
+  }
+  if (e != cudaSuccess || p.S == 1) return e;
+  return launch_dep(qgemm_i8_reduce_kernel,
+                    dim3((unsigned)((p.units - p.full) / p.S), (unsigned)((p.NB + kI8ReduceRows - 1) / kI8ReduceRows)),
+                    dim3(256), 0, stream, p);
 }
 
 }  // namespace qg

@@ -26,18 +26,20 @@ struct I8Params {
   const uint8_t* const* codes_tab[2];
   const float* const* scales_tab[2];
   // Tiling (i8_plan)
-  int tiles;        // 128-channel tiles
+  int pair;         // CTA pairs: tiles of 256 channels x 256 rows
+  int tiles;        // channel tiles
   int NB;           // rows of x per unit at most (MMA N), a multiple of 16
   int box;          // rows per TMA box
   int b_tiles;      // row tiles of a plain call (routed: of an expert, at most)
-  int S;            // K ranges; above 1 the kernel writes int32 partials to ws
-  int units, stages, stage_bytes, tmem_cols;
+  int units, full;  // plain: units; the first `full` take all of K, those after write partials
+  int S;            // K ranges of a split tile
+  int stages, stage_bytes, tmem_cols;
   int w_again;      // a weight tile is read by more than one unit
-  int* ws;          // [S][M][N]
+  int* ws;          // partials [units - full][NB][channels of a tile]
 };
 
 void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params* p);
 size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M);
-cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map, cudaStream_t stream);
+cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorMap& map_w, cudaStream_t stream);
 
 }  // namespace qg
