@@ -33,11 +33,8 @@ cudaError_t launch_pack(int fmt, const float* W, int64_t N, int64_t K, void* cod
                         float* tensor_scale, cudaStream_t stream);
 cudaError_t launch_repack(const RepackParams& rp, cudaStream_t stream);
 cudaError_t launch_reduce(const ReduceParams& rp, cudaStream_t stream);
-size_t moe_sort_bytes(int64_t S, int E);
-cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, int* hist,
-                            cudaStream_t stream);
-cudaError_t launch_moe_gather(const void* x, int64_t T, int64_t row_bytes, int k, const int* row,
-                              void* xs, cudaStream_t stream);
+cudaError_t launch_moe_dispatch(const void* x, int64_t T, int64_t row_bytes, const int* ids, int k,
+                                int E, int* offsets, int* row, void* xs, cudaStream_t stream);
 cudaError_t launch_moe_combine(bool in_bf16, bool out_bf16, const void* ys, int64_t T, int64_t H,
                                int k, const int* row, const float* w, void* y, cudaStream_t stream);
 cudaError_t launch_moe_combine_grad(bool dy_bf16, bool ys_bf16, const void* dy, const void* ys,
@@ -1120,18 +1117,8 @@ int check_routed(int64_t T, int k, int64_t H) {
 }
 }  // namespace
 
-int qgemm_moe_dispatch_workspace_size(int64_t T, int k, int E, size_t* bytes) {
-  const int st = check_routed(T, k, 1);
-  if (st != QGEMM_OK) return st;
-  if (E < 1 || E > QGEMM_MOE_MAX_EXPERTS) return QGEMM_ERR_SHAPE;
-  if (!bytes) return QGEMM_ERR_NULL;
-  *bytes = moe_sort_bytes(T * k, E);
-  return QGEMM_OK;
-}
-
 int qgemm_moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, const int32_t* experts, int k,
-                       int E, int32_t* offsets, int32_t* rows, void* xs, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+                       int E, int32_t* offsets, int32_t* rows, void* xs, void* stream) {
   if (!row_dtype(dtype)) return QGEMM_ERR_FORMAT;
   const int st = check_routed(T, k, H);
   if (st != QGEMM_OK) return st;
@@ -1139,15 +1126,10 @@ int qgemm_moe_dispatch(const void* x, int dtype, int64_t T, int64_t H, const int
   if (!x || !experts || !offsets || !rows || !xs) return QGEMM_ERR_NULL;
   if (!aligned16(x) || !aligned16(xs) || !aligned4(experts) || !aligned4(offsets) || !aligned4(rows))
     return QGEMM_ERR_ALIGN;
-  const size_t need = moe_sort_bytes(T * k, E);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return QGEMM_ERR_WORKSPACE;
-  if (workspace && !aligned16(workspace)) return QGEMM_ERR_ALIGN;
   if (!device_ok()) return QGEMM_ERR_DEVICE;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_moe_sort(experts, T * k, E, offsets, rows, static_cast<int*>(workspace), s);
-  if (e != cudaSuccess) return cuda_fail(e, "expert sort launch");
-  e = launch_moe_gather(x, T, H * (dtype == QGEMM_Y_BF16 ? 2 : 4), k, rows, xs, s);
-  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "row gather launch");
+  const cudaError_t e = launch_moe_dispatch(x, T, H * (dtype == QGEMM_Y_BF16 ? 2 : 4), experts, k, E, offsets, rows,
+                                            xs, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "dispatch launch");
 }
 
 int qgemm_moe_dispatch_grad(const void* dxs, int dxs_dtype, int64_t T, int64_t H, const int32_t* rows,

@@ -41,36 +41,13 @@ static cudaError_t launch_dep(void (*kern)(P...), dim3 grid, dim3 block, size_t 
 // ---------------------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------------------
-constexpr int kSortThreads = 256;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortChunk = 1024;   // slots per block, while that needs at most kSortBlocks blocks
-constexpr int kSortBlocks = 148;
+constexpr int kSmallSlots = 4096;  // up to here one launch dispatches
+constexpr int kSmallThreads = 256;
+constexpr int kSortCtas = 8;       // a portable cluster
+constexpr int kSortMaxWarps = 16;
 
-struct SortParams {
-  const int* ids;  // [S]
-  int S, E, nb, chunk;
-  int* hist;       // [nb][E]: slots of each expert in each block's chunk
-  int* offsets;    // [E + 1]
-  int* row;        // [S]
-};
-
-__global__ void __launch_bounds__(kSortThreads) qgemm_moe_count_kernel(const SortParams p) {
-  extern __shared__ int sm_hist[];
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int e = threadIdx.x; e < p.E; e += kSortThreads) sm_hist[e] = 0;
-  __syncthreads();
-  const int64_t s0 = (int64_t)blockIdx.x * p.chunk;
-  const int n = (int)min((int64_t)p.chunk, (int64_t)p.S - s0);
-  for (int i = threadIdx.x; i < n; i += kSortThreads) {
-    const int e = p.ids[s0 + i];
-    if ((unsigned)e < (unsigned)p.E) atomicAdd(&sm_hist[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kSortThreads) p.hist[(size_t)blockIdx.x * p.E + e] = sm_hist[e];
-}
-
-// Exclusive prefix sum of v over the block's threads, in thread order; *total gets the sum.
+// Exclusive prefix sum of v over the block's threads (whole warps, at most kSortMaxWarps), in thread
+// order; *total gets the sum.  red: an int per warp.
 __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int inc = v;
@@ -82,8 +59,7 @@ __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
   if (lane == 31) red[w] = inc;
   __syncthreads();
   int base = 0, sum = 0;
-#pragma unroll
-  for (int i = 0; i < kSortWarps; ++i) {
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
     if (i < w) base += red[i];
     sum += red[i];
   }
@@ -92,67 +68,166 @@ __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
   return base + inc - v;
 }
 
-// Rows of one chunk.  Shared memory: the running row of each expert for each warp's share of the
-// chunk, [kSortWarps][E].
-__global__ void __launch_bounds__(kSortThreads) qgemm_moe_rank_kernel(const SortParams p) {
+// Few slots: one launch for everything.  A block is a token: the row of each of its slots is a count over
+// all slots of those that come before it in the order (expert, slot), read as one integer key; then the
+// block copies the token's row to its places.  The last block counts the offsets.  (This kernel does
+// not let its dependents launch early: qgemm_moe_run reads the offsets before it waits for the grid
+// ahead of it.)
+template <typename V>
+__global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel(
+    const int* __restrict__ ids, int T, int k, int E, const V* __restrict__ x, int nvec, int* __restrict__ offsets,
+    int* __restrict__ row, V* __restrict__ xs) {
+  extern __shared__ int sm_hist[];
+  __shared__ int red[kSmallThreads / 32][8];
+  __shared__ int place[8];
+  griddep_wait();
+  const int S = T * k, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  if ((int)blockIdx.x == T) {
+    for (int e = tid; e < E; e += kSmallThreads) sm_hist[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < S; i += kSmallThreads) {
+      const int e = ids[i];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&sm_hist[e], 1);
+    }
+    __syncthreads();
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += kSmallThreads) {
+      const int e = e0 + tid;
+      int sum;
+      const int first = carry + block_excl_scan(e < E ? sm_hist[e] : 0, &red[0][0], &sum);
+      carry += sum;
+      if (e < E) offsets[e] = first;
+    }
+    if (tid == 0) offsets[E] = carry;
+    return;
+  }
+  const int t = blockIdx.x;
+  V a;
+  if (tid < nvec) a = x[(int64_t)t * nvec + tid];
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int key[8], cnt[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = j0 + j < k ? __ldg(ids + t * k + j0 + j) : -1;
+      key[j] = (unsigned)e < (unsigned)E ? e * kSmallSlots + (t * k + j0 + j) : -1;
+      cnt[j] = 0;
+    }
+    for (int i = tid; i < S; i += kSmallThreads) {
+      const int e = __ldg(ids + i);
+      const int ki = (unsigned)e < (unsigned)E ? e * kSmallSlots + i : 0x7FFFFFFF;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cnt[j] += ki < key[j] ? 1 : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cnt[j] = __reduce_add_sync(0xffffffffu, cnt[j]);
+      if (lane == j) red[w][j] = cnt[j];
+    }
+    __syncthreads();
+    if (tid < 8) {
+      int s = 0;
+#pragma unroll
+      for (int i = 0; i < kSmallThreads / 32; ++i) s += red[i][tid];
+      const int e = j0 + tid < k ? __ldg(ids + t * k + j0 + tid) : -1;
+      const int ro = (unsigned)e < (unsigned)E ? s : -1;
+      place[tid] = ro;
+      if (j0 + tid < k) row[t * k + j0 + tid] = ro;
+    }
+    __syncthreads();
+    int ro[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ro[j] = place[j];
+    for (int v = tid; v < nvec; v += kSmallThreads) {
+      const V b = v == tid ? a : x[(int64_t)t * nvec + v];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ro[j] >= 0) xs[(int64_t)ro[j] * nvec + v] = b;
+    }
+  }
+}
+
+// Many slots: one cluster of eight CTAs sorts, each a run of S / 8 slots and each warp a run of those.
+// Every warp counts its run's slots per expert; the CTAs exchange their totals through distributed shared
+// memory, so that each knows the first row of every (expert, warp); then each warp walks its run in
+// order, 32 slots at a time: a slot's row is the running row of its expert plus the lanes of the same
+// expert before it.  Shared memory: [warps][E] counts, then running rows; [E] totals of the CTA.
+// (Counts per block in global memory and a second kernel for the rows took 8 us where this takes 5, at
+// 20480 slots of 512 experts.)
+struct SortParams {
+  const int* ids;  // [S]
+  int S, E;
+  int* offsets;  // [E + 1]
+  int* row;      // [S]
+};
+
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortMaxWarps * 32)
+    qgemm_moe_sort_kernel(const SortParams p) {
   extern __shared__ int sm_cnt[];
-  __shared__ int red[kSortWarps];
+  __shared__ int red[kSortMaxWarps];
+  const int W = blockDim.x >> 5, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int rank = (int)cluster_ctarank();
+  int* tot = sm_cnt + W * p.E;
+  for (int i = threadIdx.x; i < W * p.E; i += blockDim.x) sm_cnt[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < kSortWarps * p.E; i += kSortThreads) sm_cnt[i] = 0;
   __syncthreads();
-  const int64_t s0 = (int64_t)blockIdx.x * p.chunk;
-  const int n = (int)min((int64_t)p.chunk, (int64_t)p.S - s0);
-  const int share = (n + kSortWarps - 1) / kSortWarps;
-  const int i0 = min(n, w * share), i1 = min(n, i0 + share);
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const int e = p.ids[s0 + i];
-    if ((unsigned)e < (unsigned)p.E) atomicAdd(&sm_cnt[w * p.E + e], 1);
+  const int64_t share = ((int64_t)p.S + kSortCtas * W - 1) / (kSortCtas * W);
+  const int s0 = (int)min((int64_t)p.S, share * (rank * W + w)), s1 = (int)min((int64_t)p.S, s0 + share);
+  int* cnt = sm_cnt + w * p.E;
+#pragma unroll 4
+  for (int s = s0 + lane; s < s1; s += 32) {
+    const int e = __ldg(p.ids + s);
+    if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  // first row of each expert in this chunk: all slots of smaller experts, then those of this
-  // expert in earlier chunks, then in earlier warps
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    int sum = 0;
+    for (int i = 0; i < W; ++i) sum += sm_cnt[i * p.E + e];
+    tot[e] = sum;
+  }
+  cluster_sync_all();
   int carry = 0;
-  for (int e0 = 0; e0 < p.E; e0 += kSortThreads) {
+  for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
-    int tot = 0, before = 0;
-    if (e < p.E)
-      for (int b = 0; b < p.nb; ++b) {
-        const int c = p.hist[(size_t)b * p.E + e];
-        before += (b < (int)blockIdx.x) ? c : 0;
-        tot += c;
+    int all = 0, before = 0;
+    if (e < p.E) {
+      const uint32_t a = smem_u32(tot + e);
+      int c[kSortCtas];
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r)
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[r]) : "r"(mapa_shared(a, r)) : "memory");
+#pragma unroll
+      for (int r = 0; r < kSortCtas; ++r) {
+        before += r < rank ? c[r] : 0;
+        all += c[r];
       }
+    }
     int sum;
-    const int first = carry + block_excl_scan(tot, red, &sum);
+    const int first = carry + block_excl_scan(all, red, &sum);
     carry += sum;
     if (e < p.E) {
       int at = first + before;
-#pragma unroll
-      for (int i = 0; i < kSortWarps; ++i) {
+      for (int i = 0; i < W; ++i) {
         const int c = sm_cnt[i * p.E + e];
         sm_cnt[i * p.E + e] = at;
         at += c;
       }
-      if (blockIdx.x == 0) p.offsets[e] = first;
+      if (rank == 0) p.offsets[e] = first;
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.E] = carry;
-  __syncthreads();
-  // 32 slots at a time, in order: a slot's row is the expert's running row plus the lanes of the
-  // same expert before it
-  int* cnt = sm_cnt + w * p.E;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const int e = in ? p.ids[s0 + i + lane] : -1;
+  if (rank == 0 && threadIdx.x == 0) p.offsets[p.E] = carry;
+  cluster_sync_all();  // (also: no CTA leaves while another reads its totals)
+  for (int s = s0; s < s1; s += 32) {
+    const bool in = s + lane < s1;
+    const int e = in ? __ldg(p.ids + s + lane) : -1;
     const bool ok = (unsigned)e < (unsigned)p.E;
     const unsigned same = __match_any_sync(0xffffffffu, ok ? e : -1);
-    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int before = __popc(same & ((1u << lane) - 1u));
     const int base = ok ? cnt[e] : 0;
     __syncwarp();
-    if (ok && rank == 0) cnt[e] = base + __popc(same);
+    if (ok && before == 0) cnt[e] = base + __popc(same);
     __syncwarp();
-    if (in) p.row[s0 + i + lane] = ok ? base + rank : -1;
+    if (in) p.row[s + lane] = ok ? base + before : -1;
   }
 }
 
@@ -160,6 +235,7 @@ __global__ void __launch_bounds__(kSortThreads) qgemm_moe_rank_kernel(const Sort
 // Rows.  A thread block is bx threads along a row (bx a power of two) times by tokens.
 // ---------------------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
+constexpr int kSMs = 148;  // of a B200, for the rule that spreads few tokens
 
 struct RowShape {
   int bx, by;
@@ -189,75 +265,91 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_gather_kernel(const V* 
   }
 }
 
-// N elements of a row as fp32, and back with one rounding.
-template <typename T, int N>
-struct Vec;
-template <int N>
-struct Vec<float, N> {
-  static __device__ __forceinline__ void load(const float* p, float (&f)[N]) {
-    if constexpr (N % 4 == 0) {
+// N elements of a row: raw bits as loaded (so that several rows' loads are in flight before any is
+// used), their fp32 values, and back with one rounding.
+template <int BYTES>
+struct Raw {
+  static constexpr int kWords = (BYTES + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p + i);
-        f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = p[i];
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[N]) {
-    if constexpr (N % 4 == 0) {
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (BYTES % 16 == 0) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+      for (int i = 0; i < BYTES / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (BYTES == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (BYTES == 4) {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = f[i];
-    }
-  }
-};
-template <int N>
-struct Vec<__nv_bfloat16, N> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[N]) {
-    if constexpr (N == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else if constexpr (N == 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-      f[0] = __uint_as_float(w << 16);
-      f[1] = __uint_as_float(w & 0xFFFF0000u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = __bfloat162float(p[i]);
-    }
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[N]) {
-    if constexpr (N % 2 == 0) {
-      uint32_t w[N / 2];
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      else *reinterpret_cast<uint32_t*>(p) = w[0];
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = __float2bfloat16_rn(f[i]);
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     }
   }
 };
 
+template <typename T, int N>
+struct Vec;
+template <int N>
+struct Vec<float, N> {
+  using R = Raw<4 * N>;
+  static __device__ __forceinline__ void open(const R& r, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __uint_as_float(r.w[i]);
+  }
+  static __device__ __forceinline__ R close(const float (&f)[N]) {
+    R r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = __float_as_uint(f[i]);
+    return r;
+  }
+};
+template <int N>
+struct Vec<__nv_bfloat16, N> {
+  using R = Raw<2 * N>;
+  static __device__ __forceinline__ void open(const R& r, float (&f)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      f[i] = __uint_as_float((i & 1) ? (r.w[i >> 1] & 0xFFFF0000u) : (r.w[i >> 1] << 16));
+  }
+  static __device__ __forceinline__ R close(const float (&f)[N]) {
+    R r;
+    if constexpr (N == 1) {
+      r.w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    return r;
+  }
+};
+
 // y[t] = sum_j w[t][j] ys[row[t][j]], j ascending (w absent: 1); a row outside [0, S) is none.
-template <typename TI, typename TO, int N>
+// The loads of `per` slots (at most B) go together: k in equal batches.
+template <typename TI, typename TO, int N, int B>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI* __restrict__ ys, int64_t T,
-                                                                        int H, int k, int64_t S,
+                                                                        int H, int k, int per, int64_t S,
                                                                         const int* __restrict__ row,
                                                                         const float* __restrict__ w,
                                                                         TO* __restrict__ y) {
@@ -266,137 +358,137 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI
   const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;
   const int* r = row + t * k;
-  for (int h = threadIdx.x * N; h < H; h += blockDim.x * N) {
+  const float* wt = w ? w + t * k : nullptr;
+  for (int h = (blockIdx.y * blockDim.x + threadIdx.x) * N; h < H; h += gridDim.y * blockDim.x * N) {
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int ro = __ldg(r + j);
-      if (ro < 0 || ro >= S) continue;
-      const float wj = w ? __ldg(w + t * k + j) : 1.f;
-      float f[N];
-      Vec<TI, N>::load(ys + (int64_t)ro * H + h, f);
+    for (int j0 = 0; j0 < k; j0 += per) {
+      typename Vec<TI, N>::R raw[B];
+      float wj[B];
+      bool has[B];
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+      for (int j = 0; j < B; ++j) {
+        const bool in = j < per && j0 + j < k;
+        const int ro = in ? __ldg(r + j0 + j) : -1;
+        has[j] = ro >= 0 && ro < S;
+        wj[j] = has[j] && wt ? __ldg(wt + j0 + j) : 1.f;
+        raw[j].clear();
+        if (has[j]) raw[j].load(ys + (int64_t)ro * H + h);
+      }
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        if (!has[j]) continue;
+        float f[N];
+        Vec<TI, N>::open(raw[j], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+      }
     }
-    Vec<TO, N>::store(y + t * H + h, acc);
+    Vec<TO, N>::close(acc).store(y + t * H + h);
   }
 }
 
-constexpr int kGradSlots = 8;  // slots of a token whose dot products run together
+// dys[row] = w dy and dw = <dy, ys[row]>: a warp per slot (the k warps of a token find its dy in L1).
+// A lane sums its elements in ascending order, the lanes are added in a fixed tree.
+constexpr int kGradSteps = 4;  // steps of a row loaded together
 
-// dys[row] = w dy and dw = <dy, ys[row]>.  Each thread sums its elements of the row in ascending
-// order; lanes, then warps, are added in a fixed tree.
 template <typename TD, typename TY, int N>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_grad_kernel(
-    const TD* __restrict__ dy, const TY* __restrict__ ys, int64_t T, int H, int k, int64_t S,
-    const int* __restrict__ row, const float* __restrict__ w, TY* __restrict__ dys, float* __restrict__ dw) {
-  __shared__ float red[kRowThreads / 32][kGradSlots];
+    const TD* __restrict__ dy, const TY* __restrict__ ys, int64_t S, int H, int k, const int* __restrict__ row,
+    const float* __restrict__ w, TY* __restrict__ dys, float* __restrict__ dw) {
   griddep_wait();
   griddep_launch_dependents();
-  const int bx = blockDim.x;
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = t < T;  // (every thread takes part in the reductions)
-  const int tid = threadIdx.y * bx + threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int j0 = 0; j0 < k; j0 += kGradSlots) {
-    int ro[kGradSlots];
-    float wj[kGradSlots], part[kGradSlots];
+  const int64_t s = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (s >= S) return;
+  const int ro = __ldg(row + s);
+  if (ro < 0 || ro >= S) {
+    if (lane == 0) dw[s] = 0.f;
+    return;
+  }
+  const float ws = __ldg(w + s);
+  const TD* d0 = dy + s / k * H;
+  const TY* y0 = ys + (int64_t)ro * H;
+  TY* o0 = dys + (int64_t)ro * H;
+  float part = 0.f;
+  for (int h0 = lane * N; h0 < H; h0 += kGradSteps * 32 * N) {
+    typename Vec<TD, N>::R rd[kGradSteps];
+    typename Vec<TY, N>::R ry[kGradSteps];
 #pragma unroll
-    for (int j = 0; j < kGradSlots; ++j) {
-      ro[j] = (live && j0 + j < k) ? __ldg(row + t * k + j0 + j) : -1;
-      if (ro[j] >= S) ro[j] = -1;
-      wj[j] = ro[j] >= 0 ? __ldg(w + t * k + j0 + j) : 0.f;
-      part[j] = 0.f;
+    for (int i = 0; i < kGradSteps; ++i) {
+      const int h = h0 + i * 32 * N;
+      rd[i].clear();
+      ry[i].clear();
+      if (h < H) {
+        rd[i].load(d0 + h);
+        ry[i].load(y0 + h);
+      }
     }
-    if (live)
-      for (int h = threadIdx.x * N; h < H; h += bx * N) {
-        float d[N];
-        Vec<TD, N>::load(dy + t * H + h, d);
 #pragma unroll
-        for (int j = 0; j < kGradSlots; ++j) {
-          if (ro[j] < 0) continue;
-          float f[N], g[N];
-          Vec<TY, N>::load(ys + (int64_t)ro[j] * H + h, f);
+    for (int i = 0; i < kGradSteps; ++i) {
+      const int h = h0 + i * 32 * N;
+      float d[N], f[N];
+      Vec<TD, N>::open(rd[i], d);
+      Vec<TY, N>::open(ry[i], f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            part[j] = fmaf(d[i], f[i], part[j]);
-            g[i] = wj[j] * d[i];
-          }
-          Vec<TY, N>::store(dys + (int64_t)ro[j] * H + h, g);
-        }
+      for (int e = 0; e < N; ++e) {
+        part = fmaf(d[e], f[e], part);
+        d[e] *= ws;
       }
-    const int width = min(bx, 32);
-#pragma unroll
-    for (int j = 0; j < kGradSlots; ++j)
-      for (int o = width >> 1; o > 0; o >>= 1) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
-    if (bx > 32) {
-      if (lane == 0)
-#pragma unroll
-        for (int j = 0; j < kGradSlots; ++j) red[warp][j] = part[j];
-      __syncthreads();
-      const int w0 = threadIdx.y * (bx >> 5);
-      if (threadIdx.x < kGradSlots) {
-        float s = 0.f;
-        for (int i = 0; i < (bx >> 5); ++i) s += red[w0 + i][threadIdx.x];
-        if (live && j0 + (int)threadIdx.x < k) dw[t * k + j0 + threadIdx.x] = s;
-      }
-      __syncthreads();
-    } else if (live && threadIdx.x == 0) {
-#pragma unroll
-      for (int j = 0; j < kGradSlots; ++j)
-        if (j0 + j < k) dw[t * k + j0 + j] = part[j];
+      if (h < H) Vec<TY, N>::close(d).store(o0 + h);
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+  if (lane == 0) dw[s] = part;
 }
 
 // ---------------------------------------------------------------------------------------
 // Host-side launchers
 // ---------------------------------------------------------------------------------------
-static int sort_chunk(int64_t S) {
-  return (int)std::max<int64_t>(kSortChunk, (S + kSortBlocks - 1) / kSortBlocks);
-}
-
-size_t moe_sort_bytes(int64_t S, int E) {
-  const int64_t c = sort_chunk(S);
-  return (size_t)((S + c - 1) / c) * (size_t)E * 4;
-}
-
-cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, int* hist,
-                            cudaStream_t stream) {
-  SortParams p{};
-  p.ids = ids;
-  p.S = (int)S;
-  p.E = E;
-  p.chunk = sort_chunk(S);
-  p.nb = (int)((S + p.chunk - 1) / p.chunk);
-  p.hist = hist;
-  p.offsets = offsets;
-  p.row = row;
-  const size_t rank_smem = (size_t)kSortWarps * E * 4;
-  if (rank_smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(qgemm_moe_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+static cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, cudaStream_t stream) {
+  const SortParams p{ids, (int)S, E, offsets, row};
+  // as many warps as have their counts in shared memory (all 16 up to 3328 experts)
+  const int warps = std::min(kSortMaxWarps, (kSmemLimit - 1024) / (4 * E) - 1);
+  const size_t smem = (size_t)(warps + 1) * E * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(qgemm_moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemLimit - 1024);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = launch_dep(qgemm_moe_count_kernel, dim3(p.nb), dim3(kSortThreads), (size_t)E * 4, stream, p);
-  if (e != cudaSuccess) return e;
-  return launch_dep(qgemm_moe_rank_kernel, dim3(p.nb), dim3(kSortThreads), rank_smem, stream, p);
+  return launch_dep(qgemm_moe_sort_kernel, dim3(kSortCtas), dim3(warps * 32), smem, stream, p);
 }
 
 template <typename V>
-static cudaError_t gather_impl(const void* x, int64_t T, int64_t row_bytes, int k, const int* row, void* xs,
-                               cudaStream_t stream) {
+static cudaError_t dispatch_impl(const void* x, int64_t T, int64_t row_bytes, const int* ids, int k, int E,
+                                 int* offsets, int* row, void* xs, cudaStream_t stream) {
   const int nvec = (int)(row_bytes / (int64_t)sizeof(V));
+  const V* xv = static_cast<const V*>(x);
+  V* xsv = static_cast<V*>(xs);
+  if (T * k <= kSmallSlots)
+    return launch_dep(qgemm_moe_dispatch_small_kernel<V>, dim3((unsigned)T + 1), dim3(kSmallThreads), (size_t)E * 4,
+                      stream, ids, (int)T, k, E, xv, nvec, offsets, row, xsv);
+  const cudaError_t e = launch_moe_sort(ids, T * k, E, offsets, row, stream);
+  if (e != cudaSuccess) return e;
   const RowShape s = row_shape(nvec);
   return launch_dep(qgemm_moe_gather_kernel<V>, dim3((unsigned)((T + s.by - 1) / s.by)), dim3(s.bx, s.by), 0,
-                    stream, static_cast<const V*>(x), T, nvec, k, row, static_cast<V*>(xs));
+                    stream, xv, T, nvec, k, (const int*)row, xsv);
 }
 
-cudaError_t launch_moe_gather(const void* x, int64_t T, int64_t row_bytes, int k, const int* row, void* xs,
-                              cudaStream_t stream) {
-  if (row_bytes % 16 == 0) return gather_impl<uint4>(x, T, row_bytes, k, row, xs, stream);
-  if (row_bytes % 4 == 0) return gather_impl<uint32_t>(x, T, row_bytes, k, row, xs, stream);
-  return gather_impl<uint16_t>(x, T, row_bytes, k, row, xs, stream);
+cudaError_t launch_moe_dispatch(const void* x, int64_t T, int64_t row_bytes, const int* ids, int k, int E,
+                                int* offsets, int* row, void* xs, cudaStream_t stream) {
+  if (row_bytes % 16 == 0)
+    return dispatch_impl<uint4>(x, T, row_bytes, ids, k, E, offsets, row, xs, stream);
+  if (row_bytes % 4 == 0)
+    return dispatch_impl<uint32_t>(x, T, row_bytes, ids, k, E, offsets, row, xs, stream);
+  return dispatch_impl<uint16_t>(x, T, row_bytes, ids, k, E, offsets, row, xs, stream);
+}
+
+// k slots in equal batches of at most b.
+static int batch_of(int k, int b) {
+  const int n = (k + b - 1) / b;
+  return (k + n - 1) / n;
 }
 
 // Elements per thread and step: 8 (16 bytes of bf16) where H allows it, else 2, else 1 -- rows
@@ -408,15 +500,27 @@ static cudaError_t by_width(int64_t H, F f) {
   return f(std::integral_constant<int, 1>{});
 }
 
+template <typename TI, typename TO, int N, int B>
+static cudaError_t combine_batch(const void* ys, int64_t T, int64_t H, int k, const int* row, const float* w,
+                                 void* y, cudaStream_t stream) {
+  const RowShape s = row_shape(H / N);
+  const int64_t blocks = (T + s.by - 1) / s.by;
+  // few tokens: the pieces of a row go to blocks of their own
+  const int64_t pieces = (H / N + s.bx - 1) / s.bx;
+  const unsigned gy = (unsigned)(blocks < 2 * kSMs ? std::min<int64_t>(pieces, 64) : 1);
+  return launch_dep(qgemm_moe_combine_kernel<TI, TO, N, B>, dim3((unsigned)blocks, gy), dim3(s.bx, s.by), 0, stream,
+                    static_cast<const TI*>(ys), T, (int)H, k, batch_of(k, B), T * k, row, w, static_cast<TO*>(y));
+}
+
 template <typename TI, typename TO>
 static cudaError_t combine_impl(const void* ys, int64_t T, int64_t H, int k, const int* row, const float* w,
                                 void* y, cudaStream_t stream) {
   return by_width(H, [&](auto n) {
     constexpr int N = decltype(n)::value;
-    const RowShape s = row_shape(H / N);
-    return launch_dep(qgemm_moe_combine_kernel<TI, TO, N>, dim3((unsigned)((T + s.by - 1) / s.by)),
-                      dim3(s.bx, s.by), 0, stream, static_cast<const TI*>(ys), T, (int)H, k, T * k, row, w,
-                      static_cast<TO*>(y));
+    // registers for no more slots than a batch has: two slots in the registers of eight ran 35 % slower
+    if (k <= 2) return combine_batch<TI, TO, N, 2>(ys, T, H, k, row, w, y, stream);
+    if (k <= 4 || (N == 8 && sizeof(TI) == 4)) return combine_batch<TI, TO, N, 4>(ys, T, H, k, row, w, y, stream);
+    return combine_batch<TI, TO, N, 8>(ys, T, H, k, row, w, y, stream);
   });
 }
 
@@ -435,10 +539,10 @@ static cudaError_t combine_grad_impl(const void* dy, const void* ys, int64_t T, 
                                      const float* w, void* dys, float* dw, cudaStream_t stream) {
   return by_width(H, [&](auto n) {
     constexpr int N = decltype(n)::value;
-    const RowShape s = row_shape(H / N);
-    return launch_dep(qgemm_moe_combine_grad_kernel<TD, TY, N>, dim3((unsigned)((T + s.by - 1) / s.by)),
-                      dim3(s.bx, s.by), 0, stream, static_cast<const TD*>(dy), static_cast<const TY*>(ys), T,
-                      (int)H, k, T * k, row, w, static_cast<TY*>(dys), dw);
+    constexpr int kWarps = kRowThreads / 32;
+    return launch_dep(qgemm_moe_combine_grad_kernel<TD, TY, N>, dim3((unsigned)((T * k + kWarps - 1) / kWarps)),
+                      dim3(kRowThreads), 0, stream, static_cast<const TD*>(dy), static_cast<const TY*>(ys), T * k,
+                      (int)H, k, row, w, static_cast<TY*>(dys), dw);
   });
 }
 

@@ -59,8 +59,7 @@ SIGNATURES = [
     ("qgemm_bs_ffn_workspace_size", _I, [_I, _I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     ("qgemm_bs_ffn_gate_up", _I, [_I, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP,
                                   _VP, _SZ, _VP]),
-    ("qgemm_moe_dispatch_workspace_size", _I, [_I64, _I, _I, ctypes.POINTER(_SZ)]),
-    ("qgemm_moe_dispatch", _I, [_VP, _I, _I64, _I64, _VP, _I, _I, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    ("qgemm_moe_dispatch", _I, [_VP, _I, _I64, _I64, _VP, _I, _I, _VP, _VP, _VP, _VP]),
     ("qgemm_moe_dispatch_grad", _I, [_VP, _I, _I64, _I64, _VP, _I, _VP, _I, _VP]),
     ("qgemm_moe_combine", _I, [_VP, _I, _I64, _I64, _VP, _VP, _I, _VP, _I, _VP]),
     ("qgemm_moe_combine_grad", _I, [_VP, _I, _VP, _I, _I64, _I64, _VP, _VP, _I, _VP, _VP, _VP]),
@@ -458,17 +457,8 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-@functools.lru_cache(maxsize=256)
-def moe_dispatch_workspace_size(T: int, k: int, E: int) -> int:
-    b = _SZ()
-    _check(lib().qgemm_moe_dispatch_workspace_size(T, k, E, ctypes.byref(b)),
-           "qgemm_moe_dispatch_workspace_size")
-    return b.value
-
-
 def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tensor | None = None,
-                 offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None,
-                 workspace=None, stream=None):
+                 offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None, stream=None):
     """qgemm_moe_dispatch: tokens x [T, H] (bf16 or fp32) and their experts int32 [T, k] (outside
     [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
     T, H = x.shape
@@ -487,13 +477,9 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
         rows = torch.empty((T, k), dtype=torch.int32, device=x.device)
     else:
         assert rows.dtype == torch.int32 and rows.shape == (T, k)
-    if workspace is None:
-        nbytes = moe_dispatch_workspace_size(T, k, E)
-        workspace = _scratch(nbytes, x.device, stream) if nbytes else None
-    guard, st = _at(stream, x, experts, xs, offsets, rows, *(() if workspace is None else (workspace,)))
+    guard, st = _at(stream, x, experts, xs, offsets, rows)
     _call("qgemm_moe_dispatch", guard, x.data_ptr(), dt, T, H, experts.data_ptr(), k, E, offsets.data_ptr(),
-          rows.data_ptr(), xs.data_ptr(), None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else _nbytes(workspace), st)
+          rows.data_ptr(), xs.data_ptr(), st)
     return xs, offsets, rows
 
 

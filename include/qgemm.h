@@ -344,7 +344,6 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
  *               of qgemm_moe_run; offsets[E] slots have a row);
  *   xs_dev      [T k][H]: xs[rows[t][j]] = x[t] bit for bit.  Rows from offsets[E] on are left as
  *               they were.
- * Workspace: qgemm_moe_dispatch_workspace_size() bytes, no initialisation.
  *
  * qgemm_moe_combine:       y[t] = sum_j weights[t][j] * ys[rows[t][j]], j ascending.
  * qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t][j]] (the gradient of x given that of xs).
@@ -354,15 +353,13 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
  * ys, dys, dxs hold T k rows; a value of rows_dev outside [0, T k) counts as -1, and no two slots
  * may name one row in qgemm_moe_combine_grad.  A slot without a row is not read: what its weight
  * or a row behind the last expert holds, NaN included, reaches no output.
- * Errors: QGEMM_ERR_FORMAT (types), _SHAPE, _NULL, _ALIGN, _WORKSPACE, _DEVICE, _CUDA.
+ * Errors: QGEMM_ERR_FORMAT (types), _SHAPE, _NULL, _ALIGN, _DEVICE, _CUDA.
  */
 #define QGEMM_MOE_MAX_EXPERTS 4096
 
-int qgemm_moe_dispatch_workspace_size(int64_t T, int k, int E, size_t* bytes);
 int qgemm_moe_dispatch(const void* x_dev, int dtype, int64_t T, int64_t H,
                        const int32_t* experts_dev, int k, int E, int32_t* offsets_dev,
-                       int32_t* rows_dev, void* xs_dev, void* workspace, size_t workspace_bytes,
-                       void* stream);
+                       int32_t* rows_dev, void* xs_dev, void* stream);
 int qgemm_moe_dispatch_grad(const void* dxs_dev, int dxs_dtype, int64_t T, int64_t H,
                             const int32_t* rows_dev, int k, void* dx_dev, int dx_dtype,
                             void* stream);

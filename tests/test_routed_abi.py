@@ -17,8 +17,8 @@ def lib():
     return qgemm.lib()
 
 
-def _dispatch(lib, x=16, dt=1, T=4, H=64, ids=16, k=2, E=8, off=16, rows=16, xs=16, ws=16, n=BIG):
-    return lib.qgemm_moe_dispatch(x, dt, T, H, ids, k, E, off, rows, xs, ws, n, None)
+def _dispatch(lib, x=16, dt=1, T=4, H=64, ids=16, k=2, E=8, off=16, rows=16, xs=16):
+    return lib.qgemm_moe_dispatch(x, dt, T, H, ids, k, E, off, rows, xs, None)
 
 
 def _combine(lib, ys=16, dt=1, T=4, H=64, rows=16, w=16, k=2, y=16, ydt=1):
@@ -54,8 +54,6 @@ REFUSED = [
     (_dispatch, dict(rows=None), NULL), (_dispatch, dict(xs=None), NULL),
     (_dispatch, dict(x=8), ALIGN), (_dispatch, dict(xs=24), ALIGN), (_dispatch, dict(ids=18), ALIGN),
     (_dispatch, dict(off=18), ALIGN), (_dispatch, dict(rows=18), ALIGN),
-    (_dispatch, dict(T=8192, ws=None), WORKSPACE), (_dispatch, dict(T=8192, n=63), WORKSPACE),
-    (_dispatch, dict(T=8192, ws=24), ALIGN),
     (_combine, dict(dt=2), FORMAT), (_combine, dict(ydt=-1), FORMAT), (_combine, dict(T=0), SHAPE),
     (_combine, dict(k=0), SHAPE), (_combine, dict(H=0), SHAPE), (_combine, dict(H=1 << 31), SHAPE),
     (_combine, dict(ys=None), NULL), (_combine, dict(rows=None), NULL), (_combine, dict(w=None), NULL),
@@ -105,9 +103,6 @@ def test_sizes(lib):
     assert qgemm.i8_moe_workspace_size(512, 2048, 640) >= 640 * 2052
     assert lib.qgemm_i8_workspace_size(8, 64, 0, ctypes.byref(sz)) == SHAPE
     assert lib.qgemm_i8_moe_workspace_size(8, 64, 4, None) == NULL
-    assert lib.qgemm_moe_dispatch_workspace_size(4, 0, 8, ctypes.byref(sz)) == SHAPE
-    assert lib.qgemm_moe_dispatch_workspace_size(4, 2, 5000, ctypes.byref(sz)) == SHAPE
-    assert lib.qgemm_moe_dispatch_workspace_size(4, 2, 8, None) == NULL
     assert lib.qgemm_i8_quant_x(16, 4, 24, 16, 16, None) == K_BLOCK
     assert lib.qgemm_i8_quant_x(16, 0, 32, 16, 16, None) == SHAPE
     assert lib.qgemm_i8_quant_x(16, 4, 32, 16, None, None) == NULL
