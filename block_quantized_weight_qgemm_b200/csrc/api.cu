@@ -43,7 +43,7 @@ cudaError_t launch_moe_combine_grad(bool dy_bf16, bool ys_bf16, const void* dy, 
 cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes, float* scales,
                            cudaStream_t stream);
 cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales,
-                            cudaStream_t stream);
+                            bool early, cudaStream_t stream);
 int* device_error_word();
 }  // namespace qg
 
@@ -1228,7 +1228,7 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
     return QGEMM_ERR_CUDA;
   }
   cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, reinterpret_cast<int8_t*>(wsb),
-                                  reinterpret_cast<float*>(wsb + w.scales), s);
+                                  reinterpret_cast<float*>(wsb + w.scales), !routed, s);
   if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
   if (g_prof_begin) cudaEventRecord(g_prof_begin, s);
   e = launch_i8_gemm(p, map, map_w, s);
@@ -1286,7 +1286,7 @@ int qgemm_i8_quant_x(const void* x, int64_t M, int64_t K, void* codes, float* sc
   if (!aligned16(x) || !aligned16(codes) || !aligned4(scales)) return QGEMM_ERR_ALIGN;
   if (!device_ok()) return QGEMM_ERR_DEVICE;
   const cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, static_cast<int8_t*>(codes), scales,
-                                        static_cast<cudaStream_t>(stream));
+                                        false, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? QGEMM_OK : cuda_fail(e, "int8 quantisation launch");
 }
 

@@ -30,6 +30,7 @@ struct I8QuantParams {
   int K;
   int8_t* codes;  // [M][K]
   float* scales;  // [M]
+  int early;      // the dependent grid reads only weights before it waits
 };
 
 // Eight rounded quotients.  t = x inv + 1.5 2^23 rounds x / s to an integer (in t's low bits) up
@@ -67,10 +68,13 @@ __device__ __forceinline__ uint2 i8_codes8(const uint4& v, float up, float inv, 
 // Per row: the largest |x| as bf16 bits (which order like the magnitudes, infinities and NaN
 // above every finite value), the scale, the codes.
 __global__ void __launch_bounds__(kI8QuantThreads) qgemm_i8_quant_kernel(const I8QuantParams p) {
-  // x may come from the grid before this one; only once that has completed may the GEMM launch,
-  // which reads weights, offsets and tables before it waits for this grid
+  // The GEMM that follows starts its set-up and its weight copies before it waits for this grid.  A
+  // plain one reads nothing else by then, and may launch at once (weights come from a grid that has
+  // ended, as the header says); a routed one also reads offsets and tables, which the grid before
+  // this one may have written.
+  if (p.early) griddep_launch_dependents();
   griddep_wait();
-  griddep_launch_dependents();
+  if (!p.early) griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const int step = blockDim.x * 8;
   const uint16_t* xr = p.x + m * p.K;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(256) qgemm_i8_pack_kernel(const float* __restr
 // ---------------------------------------------------------------------------------------
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
-constexpr int kI8Strip = 128;  // row scales per epilogue warp: half of a unit's 256 rows
+constexpr int kI8Strip = 128;  // rows per epilogue warp: half of a unit's 256 at most
 constexpr int kI8MaxStages = 12;
 constexpr int kI8List = 128;  // units of a CTA found ahead (routed)
 
@@ -293,20 +297,20 @@ struct I8Scales {
 // ch: the lane's channel within the unit, of `width`.
 template <int NMAT>
 __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT>& V, uint32_t d, int hw, int64_t n,
-                                            int ch, int width, const float (&sw)[NMAT], const float* sxs) {
+                                            int ch, int width, const float (&sw)[NMAT],
+                                            const float (&sxl)[kI8Strip / 32]) {
   const bool in = n < p.N;
   for (int cb = hw * 16; cb < V.rows; cb += 32) {
     __syncwarp();
     uint32_t v[NMAT][16];
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) i8_tmem_ld16(d + (uint32_t)(m * p.NB + cb), v[m]);
-    const float* sxb = sxs + (cb >> 5) * 16;
+    // the block's 16 row scales, of which lane 16 (b & 1) + r of entry b >> 1 holds r
+    const int b = cb >> 5;
+    const float sxb = b < 4 ? (b < 2 ? sxl[0] : sxl[1]) : (b < 6 ? sxl[2] : sxl[3]);
     float sx[16];
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(sxb + r);
-      sx[r] = f.x, sx[r + 1] = f.y, sx[r + 2] = f.z, sx[r + 3] = f.w;
-    }
+    for (int r = 0; r < 16; ++r) sx[r] = __shfl_sync(0xffffffffu, sxb, ((b & 1) << 4) + r);
     tmem_ld_wait();
     const int nr = min(16, V.rows - cb);
     // 16 rows of one channel: a full block without a branch per row, so that its stores follow one
@@ -355,9 +359,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const uint32_t bar_drain = bar_acc_free + 16;
   int* ctl = reinterpret_cast<int*>(bars + 2 * kI8MaxStages + 6);
   volatile int* abort_flag = ctl + 1;
-  float* strip = reinterpret_cast<float*>(ctl + 4);  // [epilogue warps][kI8Strip]
   // routed: the CTA's first units, then [E] the units before each expert's
-  I8Unit<NMAT>* list = reinterpret_cast<I8Unit<NMAT>*>(strip + kI8EpiWarps * kI8Strip);
+  I8Unit<NMAT>* list = reinterpret_cast<I8Unit<NMAT>*>(ctl + 4);
   int* pre = reinterpret_cast<int*>(list + kI8List);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -531,7 +534,6 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     // loaded while the unit before it is computed and read out.
     const int q = warp & 3, hw = (warp - 2) >> 2, ch = q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    float* sxs = strip + (warp - 2) * kI8Strip;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
     I8Unit<NMAT> U;
@@ -544,19 +546,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     int i = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
       const I8Unit<NMAT> V = U;
-      float sw[NMAT];
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m) sw[m] = sc.sw[m];
-#pragma unroll
-      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sc.sx[e];
-      __syncwarp();
+      const I8Scales<NMAT> vs = sc;
       if (u + (int)gridDim.x < units) fetch(i + 1, u + gridDim.x);
       bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       i8_read_out<NMAT>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw, (int64_t)V.t * kTileRows + ch, ch,
-                        kTileRows, sw, sxs);
+                        kTileRows, vs.sw, vs.sx);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
@@ -580,7 +577,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
 // thread stands between the copies and the MMAs.
 // ---------------------------------------------------------------------------------------
 constexpr int kI8PairStage = 2 * kWCodeBytes;
-constexpr int kI8PairStages = 6;
+constexpr int kI8PairStages = 7;
 
 __device__ __forceinline__ void i8_mma_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -607,7 +604,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   const uint32_t bar_drain = bar_acc_free + 16;
   int* ctl = reinterpret_cast<int*>(bars + 2 * NST + 6);
   volatile int* abort_flag = ctl + 1;
-  float* strip = reinterpret_cast<float*>(ctl + 4);  // [epilogue warps][kI8Strip]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -720,7 +716,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     // ------------------------------------------------------------ epilogue (of this CTA's channels)
     const int q = warp & 3, hw = (warp - 2) >> 2, ch = (int)rank * kTileRows + q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    float* sxs = strip + (warp - 2) * kI8Strip;
     const uint32_t free0 = mapa_shared(bar_acc_free, 0);
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
@@ -734,17 +729,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     int i = 0;
     for (int u = pid; u < p.units; u += pairs, ++i) {
       const I8Unit<1> V = U;
-      const float sw[1] = {sc.sw[0]};
-#pragma unroll
-      for (int e = 0; e < kI8Strip / 32; ++e) sxs[32 * e + lane] = sc.sx[e];
-      __syncwarp();
+      const I8Scales<1> vs = sc;
       if (u + pairs < p.units) fetch(u + pairs);
       bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       i8_read_out<1>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
-                     2 * kTileRows, sw, sxs);
+                     2 * kTileRows, vs.sw, vs.sx);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -827,10 +819,11 @@ cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes,
   return cudaGetLastError();
 }
 
-cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales,
+cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales, bool early,
                             cudaStream_t stream) {
-  I8QuantParams p{x, (int)K, codes, scales};
-  // few rows: a thread per word, for the shortest way through a row; many: four words per thread
+  I8QuantParams p{x, (int)K, codes, scales, early ? 1 : 0};
+  // few rows: a thread per word, for the shortest way through a row; many: four words per thread (2048 x
+  // 5120: 14.4, 9.6, 7.6, 10.3 us with 1, 2, 4, 8)
   const int64_t words = K / 8, per = M <= 2 * kI8SMs ? 1 : kI8QuantRegs;
   const int threads = (int)std::min<int64_t>(kI8QuantThreads, ((words + per - 1) / per + 31) / 32 * 32);
   return launch_dep(qgemm_i8_quant_kernel, dim3((unsigned)M), dim3(threads), 0, stream, p);
@@ -918,8 +911,10 @@ static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, 
   static std::atomic<uint64_t> set_mask{0};
   const cudaError_t e = raise_smem((const void*)qgemm_i8_kernel<NMAT>, set_mask, dev);
   if (e != cudaSuccess) return e;
-  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 + 4 * kI8EpiWarps * kI8Strip +
+  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 +
                       (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : 0);
+  // (a ring of half the shared memory, which lets the next product's CTAs in beside these, measured 4 to
+  // 8 % slower)
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
   // routed: an upper bound, the kernel counts the units that have rows
@@ -938,8 +933,7 @@ cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorM
     static std::atomic<uint64_t> set_mask{0};
     e = raise_smem((const void*)qgemm_i8_pair_kernel, set_mask, dev);
     if (e != cudaSuccess) return e;
-    const size_t smem = 1024 + kI8PairStages * kI8PairStage + 8 * (2 * kI8PairStages + 6) + 16 +
-                        4 * kI8EpiWarps * kI8Strip;
+    const size_t smem = 1024 + kI8PairStages * kI8PairStage + 8 * (2 * kI8PairStages + 6) + 16;
     const int grid = 2 * std::min(p.units, sm_count(dev) / 2);
     e = launch_gemm(qgemm_i8_pair_kernel, smem, grid, stream, p, map_x, map_w);
   } else {

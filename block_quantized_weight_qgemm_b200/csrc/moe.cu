@@ -41,10 +41,11 @@ static cudaError_t launch_dep(void (*kern)(P...), dim3 grid, dim3 block, size_t 
 // ---------------------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------------------
-constexpr int kSmallSlots = 4096;  // up to here one launch dispatches
+constexpr int kSmallSlots = 4096;  // up to here one launch dispatches (its work grows with the square)
 constexpr int kSmallThreads = 256;
 constexpr int kSortCtas = 8;       // a portable cluster
 constexpr int kSortMaxWarps = 16;
+constexpr int kIdLoads = 8;        // expert ids loaded together
 
 // Exclusive prefix sum of v over the block's threads (whole warps, at most kSortMaxWarps), in thread
 // order; *total gets the sum.  red: an int per warp.
@@ -73,7 +74,7 @@ __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
 // block copies the token's row to its places.  The last block counts the offsets.  (This kernel does
 // not let its dependents launch early: qgemm_moe_run reads the offsets before it waits for the grid
 // ahead of it.)
-template <typename V>
+template <typename V, int B>
 __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel(
     const int* __restrict__ ids, int T, int k, int E, const V* __restrict__ x, int nvec, int* __restrict__ offsets,
     int* __restrict__ row, V* __restrict__ xs) {
@@ -85,9 +86,16 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
   if ((int)blockIdx.x == T) {
     for (int e = tid; e < E; e += kSmallThreads) sm_hist[e] = 0;
     __syncthreads();
-    for (int i = tid; i < S; i += kSmallThreads) {
-      const int e = ids[i];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&sm_hist[e], 1);
+    for (int i0 = 0; i0 < S; i0 += kIdLoads * kSmallThreads) {
+      int e[kIdLoads];
+#pragma unroll
+      for (int q = 0; q < kIdLoads; ++q) {
+        const int i = i0 + q * kSmallThreads + tid;
+        e[q] = i < S ? __ldg(ids + i) : -1;
+      }
+#pragma unroll
+      for (int q = 0; q < kIdLoads; ++q)
+        if ((unsigned)e[q] < (unsigned)E) atomicAdd(&sm_hist[e[q]], 1);
     }
     __syncthreads();
     int carry = 0;
@@ -104,27 +112,35 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
   const int t = blockIdx.x;
   V a;
   if (tid < nvec) a = x[(int64_t)t * nvec + tid];
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    int key[8], cnt[8];
+  for (int j0 = 0; j0 < k; j0 += B) {
+    int key[B], cnt[B];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < B; ++j) {
       const int e = j0 + j < k ? __ldg(ids + t * k + j0 + j) : -1;
       key[j] = (unsigned)e < (unsigned)E ? e * kSmallSlots + (t * k + j0 + j) : -1;
       cnt[j] = 0;
     }
-    for (int i = tid; i < S; i += kSmallThreads) {
-      const int e = __ldg(ids + i);
-      const int ki = (unsigned)e < (unsigned)E ? e * kSmallSlots + i : 0x7FFFFFFF;
+    for (int i0 = 0; i0 < S; i0 += kIdLoads * kSmallThreads) {
+      int e[kIdLoads];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cnt[j] += ki < key[j] ? 1 : 0;
+      for (int q = 0; q < kIdLoads; ++q) {
+        const int i = i0 + q * kSmallThreads + tid;
+        e[q] = i < S ? __ldg(ids + i) : -1;
+      }
+#pragma unroll
+      for (int q = 0; q < kIdLoads; ++q) {
+        const int ki = (unsigned)e[q] < (unsigned)E ? e[q] * kSmallSlots + i0 + q * kSmallThreads + tid : 0x7FFFFFFF;
+#pragma unroll
+        for (int j = 0; j < B; ++j) cnt[j] += ki < key[j] ? 1 : 0;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < B; ++j) {
       cnt[j] = __reduce_add_sync(0xffffffffu, cnt[j]);
       if (lane == j) red[w][j] = cnt[j];
     }
     __syncthreads();
-    if (tid < 8) {
+    if (tid < B) {
       int s = 0;
 #pragma unroll
       for (int i = 0; i < kSmallThreads / 32; ++i) s += red[i][tid];
@@ -134,13 +150,13 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
       if (j0 + tid < k) row[t * k + j0 + tid] = ro;
     }
     __syncthreads();
-    int ro[8];
+    int ro[B];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ro[j] = place[j];
+    for (int j = 0; j < B; ++j) ro[j] = place[j];
     for (int v = tid; v < nvec; v += kSmallThreads) {
       const V b = v == tid ? a : x[(int64_t)t * nvec + v];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < B; ++j)
         if (ro[j] >= 0) xs[(int64_t)ro[j] * nvec + v] = b;
     }
   }
@@ -174,15 +190,25 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortMaxWarp
   const int64_t share = ((int64_t)p.S + kSortCtas * W - 1) / (kSortCtas * W);
   const int s0 = (int)min((int64_t)p.S, share * (rank * W + w)), s1 = (int)min((int64_t)p.S, s0 + share);
   int* cnt = sm_cnt + w * p.E;
-#pragma unroll 4
-  for (int s = s0 + lane; s < s1; s += 32) {
-    const int e = __ldg(p.ids + s);
-    if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt[e], 1);
+  auto load = [&](int s, int (&e)[kIdLoads]) {
+#pragma unroll
+    for (int q = 0; q < kIdLoads; ++q) {
+      e[q] = s + 32 * q + lane < s1 ? __ldg(p.ids + s + 32 * q + lane) : -1;
+      if ((unsigned)e[q] >= (unsigned)p.E) e[q] = -1;
+    }
+  };
+  int id[kIdLoads];
+  for (int s = s0; s < s1; s += 32 * kIdLoads) {
+    load(s, id);
+#pragma unroll
+    for (int q = 0; q < kIdLoads; ++q)
+      if (id[q] >= 0) atomicAdd(&cnt[id[q]], 1);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
     int sum = 0;
-    for (int i = 0; i < W; ++i) sum += sm_cnt[i * p.E + e];
+#pragma unroll
+    for (int i = 0; i < kSortMaxWarps; ++i) sum += i < W ? sm_cnt[i * p.E + e] : 0;
     tot[e] = sum;
   }
   cluster_sync_all();
@@ -206,28 +232,33 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortMaxWarp
     const int first = carry + block_excl_scan(all, red, &sum);
     carry += sum;
     if (e < p.E) {
-      int at = first + before;
-      for (int i = 0; i < W; ++i) {
-        const int c = sm_cnt[i * p.E + e];
-        sm_cnt[i * p.E + e] = at;
-        at += c;
+      int at = first + before, n[kSortMaxWarps];
+#pragma unroll
+      for (int i = 0; i < kSortMaxWarps; ++i) n[i] = i < W ? sm_cnt[i * p.E + e] : 0;
+#pragma unroll
+      for (int i = 0; i < kSortMaxWarps; ++i) {
+        if (i < W) sm_cnt[i * p.E + e] = at;
+        at += n[i];
       }
       if (rank == 0) p.offsets[e] = first;
     }
   }
   if (rank == 0 && threadIdx.x == 0) p.offsets[p.E] = carry;
   cluster_sync_all();  // (also: no CTA leaves while another reads its totals)
-  for (int s = s0; s < s1; s += 32) {
-    const bool in = s + lane < s1;
-    const int e = in ? __ldg(p.ids + s + lane) : -1;
-    const bool ok = (unsigned)e < (unsigned)p.E;
-    const unsigned same = __match_any_sync(0xffffffffu, ok ? e : -1);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    const int base = ok ? cnt[e] : 0;
-    __syncwarp();
-    if (ok && before == 0) cnt[e] = base + __popc(same);
-    __syncwarp();
-    if (in) p.row[s + lane] = ok ? base + before : -1;
+  for (int s = s0; s < s1; s += 32 * kIdLoads) {
+    load(s, id);
+#pragma unroll
+    for (int q = 0; q < kIdLoads; ++q) {
+      if (s + 32 * q >= s1) break;
+      const int e = id[q];
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int base = e >= 0 ? cnt[e] : 0;
+      __syncwarp();
+      if (e >= 0 && before == 0) cnt[e] = base + __popc(same);
+      __syncwarp();
+      if (s + 32 * q + lane < s1) p.row[s + 32 * q + lane] = e >= 0 ? base + before : -1;
+    }
   }
 }
 
@@ -251,13 +282,17 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_gather_kernel(const V* 
                                                                        int nvec, int k,
                                                                        const int* __restrict__ row,
                                                                        V* __restrict__ xs) {
+  // x is older than the sort, which let this grid launch after the grids before it had ended: the
+  // first piece of the row is loaded under the sort
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  V first;
+  if (t < T && threadIdx.x < nvec) first = x[t * nvec + threadIdx.x];
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t >= T) return;
   const int* r = row + t * k;
   for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-    const V a = x[t * nvec + v];
+    const V a = v == threadIdx.x ? first : x[t * nvec + v];
     for (int j = 0; j < k; ++j) {
       const int ro = __ldg(r + j);
       if (ro >= 0) xs[(int64_t)ro * nvec + v] = a;
@@ -449,7 +484,7 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_grad_kernel(
 // ---------------------------------------------------------------------------------------
 static cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, cudaStream_t stream) {
   const SortParams p{ids, (int)S, E, offsets, row};
-  // as many warps as have their counts in shared memory (all 16 up to 3328 experts)
+  // as many warps as have their counts in shared memory (all 16 up to 3400 experts)
   const int warps = std::min(kSortMaxWarps, (kSmemLimit - 1024) / (4 * E) - 1);
   const size_t smem = (size_t)(warps + 1) * E * 4;
   if (smem > 48 * 1024) {
@@ -460,15 +495,31 @@ static cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offset
   return launch_dep(qgemm_moe_sort_kernel, dim3(kSortCtas), dim3(warps * 32), smem, stream, p);
 }
 
+// k slots in equal batches of at most b.
+static int batch_of(int k, int b) {
+  const int n = (k + b - 1) / b;
+  return (k + n - 1) / n;
+}
+
 template <typename V>
 static cudaError_t dispatch_impl(const void* x, int64_t T, int64_t row_bytes, const int* ids, int k, int E,
                                  int* offsets, int* row, void* xs, cudaStream_t stream) {
   const int nvec = (int)(row_bytes / (int64_t)sizeof(V));
   const V* xv = static_cast<const V*>(x);
   V* xsv = static_cast<V*>(xs);
-  if (T * k <= kSmallSlots)
-    return launch_dep(qgemm_moe_dispatch_small_kernel<V>, dim3((unsigned)T + 1), dim3(kSmallThreads), (size_t)E * 4,
-                      stream, ids, (int)T, k, E, xv, nvec, offsets, row, xsv);
+  if (T * k <= kSmallSlots) {
+    // the slots of a token in equal batches, each counted in one pass over all slots
+    auto small = [&](auto b) {
+      return launch_dep(qgemm_moe_dispatch_small_kernel<V, decltype(b)::value>, dim3((unsigned)T + 1),
+                        dim3(kSmallThreads), (size_t)E * 4, stream, ids, (int)T, k, E, xv, nvec, offsets, row, xsv);
+    };
+    const int b = batch_of(k, 8);
+    if (b == 1) return small(std::integral_constant<int, 1>{});
+    if (b == 2) return small(std::integral_constant<int, 2>{});
+    if (b <= 4) return small(std::integral_constant<int, 4>{});
+    if (b <= 6) return small(std::integral_constant<int, 6>{});
+    return small(std::integral_constant<int, 8>{});
+  }
   const cudaError_t e = launch_moe_sort(ids, T * k, E, offsets, row, stream);
   if (e != cudaSuccess) return e;
   const RowShape s = row_shape(nvec);
@@ -483,12 +534,6 @@ cudaError_t launch_moe_dispatch(const void* x, int64_t T, int64_t row_bytes, con
   if (row_bytes % 4 == 0)
     return dispatch_impl<uint32_t>(x, T, row_bytes, ids, k, E, offsets, row, xs, stream);
   return dispatch_impl<uint16_t>(x, T, row_bytes, ids, k, E, offsets, row, xs, stream);
-}
-
-// k slots in equal batches of at most b.
-static int batch_of(int k, int b) {
-  const int n = (k + b - 1) / b;
-  return (k + n - 1) / n;
 }
 
 // Elements per thread and step: 8 (16 bytes of bf16) where H allows it, else 2, else 1 -- rows

@@ -445,9 +445,9 @@ def _call(name: str, guard, *args):
         raise QgemmError(status, name)
 
 
-def _scratch(nbytes: int, device, stream):
+def _scratch(nbytes: int, like, stream):
     """Device bytes for one call on `stream`, held until the call's work there is done."""
-    t = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    t = like.new_empty(max(nbytes, 16), dtype=torch.uint8)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -466,15 +466,15 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     dt = _ROW_DTYPES[x.dtype]
     assert T2 == T and experts.dtype == torch.int32
     if xs is None:
-        xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+        xs = x.new_empty((T * k, H))
     else:
         assert xs.dtype == x.dtype and xs.shape == (T * k, H)
     if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+        offsets = experts.new_empty(E + 1)
     else:
         assert offsets.dtype == torch.int32 and offsets.numel() == E + 1
     if rows is None:
-        rows = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        rows = torch.empty_like(experts)
     else:
         assert rows.dtype == torch.int32 and rows.shape == (T, k)
     guard, st = _at(stream, x, experts, xs, offsets, rows)
@@ -491,9 +491,9 @@ def _routed(a, rows):
     return T, k, H
 
 
-def _routed_out(out, T, H, dtype, device):
+def _routed_out(out, T, H, dtype, like):
     if out is None:
-        return torch.empty((T, H), dtype=dtype, device=device)
+        return like.new_empty((T, H), dtype=dtype)
     assert out.shape == (T, H)
     return out
 
@@ -502,7 +502,7 @@ def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | 
                       dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
     T, k, H = _routed(dxs, rows)
-    dx = _routed_out(dx, T, H, dx_dtype, dxs.device)
+    dx = _routed_out(dx, T, H, dx_dtype, dxs)
     guard, st = _at(stream, dxs, rows, dx)
     _call("qgemm_moe_dispatch_grad", guard, dxs.data_ptr(), _ROW_DTYPES[dxs.dtype], T, H, rows.data_ptr(), k,
           dx.data_ptr(), _ROW_DTYPES[dx.dtype], st)
@@ -514,7 +514,7 @@ def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
     """qgemm_moe_combine: y[t] = sum_j weights[t, j] * ys[rows[t, j]], weights fp32 [T, k]."""
     T, k, H = _routed(ys, rows)
     assert weights.dtype == torch.float32 and weights.shape == (T, k)
-    y = _routed_out(y, T, H, y_dtype, ys.device)
+    y = _routed_out(y, T, H, y_dtype, ys)
     guard, st = _at(stream, ys, rows, weights, y)
     _call("qgemm_moe_combine", guard, ys.data_ptr(), _ROW_DTYPES[ys.dtype], T, H, rows.data_ptr(),
           weights.data_ptr(), k, y.data_ptr(), _ROW_DTYPES[y.dtype], st)
@@ -527,9 +527,9 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
     moe_combine, given dy [T, H]."""
     T, k, H = _routed(ys, rows)
     assert weights.dtype == torch.float32 and weights.shape == (T, k) and dy.shape == (T, H)
-    dys = _routed_out(dys, T * k, H, ys.dtype, ys.device)
+    dys = _routed_out(dys, T * k, H, ys.dtype, ys)
     assert dys.dtype == ys.dtype
-    dw = _routed_out(dw, T, k, torch.float32, ys.device)
+    dw = _routed_out(dw, T, k, torch.float32, ys)
     assert dw.dtype == torch.float32
     guard, st = _at(stream, dy, ys, rows, weights, dys, dw)
     _call("qgemm_moe_combine_grad", guard, dy.data_ptr(), _ROW_DTYPES[dy.dtype], ys.data_ptr(),
@@ -611,9 +611,9 @@ def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=
     """qgemm_i8_run: x bf16 [M, K], quantised per row on the fly -> y [M, N] (fp32 or bf16)."""
     M, K = x.shape
     assert x.dtype == torch.bfloat16 and K == w.K
-    y = _routed_out(y, M, w.N, y_dtype, x.device)
+    y = _routed_out(y, M, w.N, y_dtype, x)
     if workspace is None:
-        workspace = _scratch(i8_workspace_size(w.N, K, M), x.device, stream)
+        workspace = _scratch(i8_workspace_size(w.N, K, M), x, stream)
     guard, st = _at(stream, x, w.codes, w.scales, y, workspace)
     _call("qgemm_i8_run", guard, x.data_ptr(), M, K, w.codes.data_ptr(), w.scales.data_ptr(), w.N, y.data_ptr(),
           _ROW_DTYPES[y.dtype], workspace.data_ptr(), _nbytes(workspace), st)
@@ -651,9 +651,9 @@ def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_r
                y: torch.Tensor | None = None, y_dtype=torch.float32, workspace=None, stream=None):
     """qgemm_i8_moe_run: rows of x grouped by expert (int32 offsets[E+1] on the device)."""
     M, K = _i8_moe(x, offsets, tab)
-    y = _routed_out(y, M, tab.N, y_dtype, x.device)
+    y = _routed_out(y, M, tab.N, y_dtype, x)
     if workspace is None:
-        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x.device, stream)
+        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x, stream)
     guard, st = _at(stream, x, offsets, tab.codes, y, workspace)
     _call("qgemm_i8_moe_run", guard, x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows,
           tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N, y.data_ptr(), _ROW_DTYPES[y.dtype],
@@ -666,10 +666,10 @@ def i8_moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: I8ExpertTable, 
     """qgemm_i8_moe_gate_up: h = bf16(SiLU(g) * u) per routed row."""
     M, K = _i8_moe(x, offsets, gate)
     assert (gate.N, gate.K, gate.E) == (up.N, up.K, up.E)
-    h = _routed_out(h, M, gate.N, torch.bfloat16, x.device)
+    h = _routed_out(h, M, gate.N, torch.bfloat16, x)
     assert h.dtype == torch.bfloat16
     if workspace is None:
-        workspace = _scratch(i8_moe_workspace_size(gate.N, K, M), x.device, stream)
+        workspace = _scratch(i8_moe_workspace_size(gate.N, K, M), x, stream)
     guard, st = _at(stream, x, offsets, gate.codes, up.codes, h, workspace)
     _call("qgemm_i8_moe_gate_up", guard, x.data_ptr(), M, K, gate.E, offsets.data_ptr(), max_rows,
           gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(),
