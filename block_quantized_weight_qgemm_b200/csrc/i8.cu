@@ -159,12 +159,14 @@ __global__ void __launch_bounds__(256) qgemm_i8_pack_kernel(const float* __restr
 //
 // Persistent, one CTA per SM.  A unit is (expert, 128-channel tile, up to NB rows, K range); two
 // accumulator sets in tensor memory let the epilogue of a unit run under the MMAs of the next.
-// Warp 0 brings each 128-K chunk into a ring of shared-memory stages (one 16 KB bulk copy per
-// matrix, one or more boxes of x), warp 1 issues four M128 N(rows) K32 MMAs per chunk and matrix,
-// warps 2..9 read the accumulators out.
+// Warp 0 brings each 128-K chunk's weights into a ring of shared-memory stages (one 16 KB bulk copy
+// per matrix) and warp 2 the rows of x (one or more boxes); apart, because the weights need not wait
+// for the quantisation kernel and fill the ring under it.  Warp 1 issues four M128 N(rows) K32 MMAs
+// per chunk and matrix, warps 3..10 read the accumulators out.
 // ---------------------------------------------------------------------------------------
 constexpr int kI8EpiWarps = 8;
-constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
+constexpr int kI8XWarp = 2, kI8EpiWarp0 = 3;
+constexpr int kI8Threads = (kI8EpiWarp0 + kI8EpiWarps) * 32;
 constexpr int kI8Strip = 128;  // rows per epilogue warp: half of a unit's 256 at most
 constexpr int kI8MaxStages = 12;
 constexpr int kI8List = 128;  // units of a CTA found ahead (routed)
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_x);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 2);  // both producers
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -432,19 +434,19 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const int set = NMAT * p.NB;  // columns of one accumulator set
   auto unit = [&](int i, int u) { return p.off && i < kI8List ? list[i] : i8_unit<NMAT>(p, pre, u); };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp == kI8XWarp) {
+    // ------------------------------------------------------------ producers: weights, rows of x
     if (lane == 0) {
-      const uint64_t pol_w = p.w_again ? policy_evict_last() : policy_evict_first();
-      const uint64_t pol_x = policy_evict_last();
+      const bool x = warp == kI8XWarp;
+      const uint64_t pol = x || p.w_again ? policy_evict_last() : policy_evict_first();
       RingPos sp;
       int issued = 0, i = 0;
-      bool ok = true, waited = false;
+      bool ok = true;
+      if (x) griddep_wait();  // the codes of x come from the preceding grid
       for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
         const I8Unit<NMAT> U = unit(i, u);
-        const int64_t n0 = (int64_t)U.t * kTileRows;
         const int boxes = (U.rows + p.box - 1) / p.box;
-        const uint32_t bytes = (uint32_t)(NMAT * kWCodeBytes + boxes * p.box * 128);
+        const uint32_t bytes = x ? (uint32_t)(boxes * p.box * 128) : (uint32_t)(NMAT * kWCodeBytes);
         for (int c = U.c0; c < U.c1; ++c) {
           if (issued >= NST &&
               !mbar_wait(bar_empty + 8 * sp.slot, sp.phase ^ 1u, abort_flag, p.dev_err, kErrTimeout)) {
@@ -454,22 +456,23 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           const uint32_t fb = bar_full + 8 * sp.slot;
           const uint32_t st = sbase + (uint32_t)(sp.slot * p.stage_bytes);
           mbar_arrive_expect_tx(fb, bytes);
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m)
-            bulk_load(st + m * kWCodeBytes, U.w[m] + ((int64_t)U.t * p.chunks + c) * kWCodeBytes, kWCodeBytes, fb,
-                      pol_w);
-          if (c == U.c0)
-            // the unit's channel scales, into L2 ahead of the epilogue
+          if (x) {
+            for (int b = 0; b < boxes; ++b)
+              i8_load_x(st + NMAT * kWCodeBytes + (uint32_t)(b * p.box * 128), &tm_x, fb, c * 128,
+                        U.row0 + b * p.box, pol);
+          } else {
 #pragma unroll
             for (int m = 0; m < NMAT; ++m)
-              for (int64_t n = n0; n < n0 + kTileRows && n < p.N; n += 32) prefetch_l2(U.sc[m] + n);
-          if (!waited) {
-            griddep_wait();  // the codes of x come from the preceding grid
-            waited = true;
+              bulk_load(st + m * kWCodeBytes, U.w[m] + ((int64_t)U.t * p.chunks + c) * kWCodeBytes, kWCodeBytes, fb,
+                        pol);
+            if (c == U.c0) {
+              // the unit's channel scales, into L2 ahead of the epilogue
+              const int64_t n0 = (int64_t)U.t * kTileRows;
+#pragma unroll
+              for (int m = 0; m < NMAT; ++m)
+                for (int64_t n = n0; n < n0 + kTileRows && n < p.N; n += 32) prefetch_l2(U.sc[m] + n);
+            }
           }
-          for (int b = 0; b < boxes; ++b)
-            i8_load_x(st + NMAT * kWCodeBytes + (uint32_t)(b * p.box * 128), &tm_x, fb, c * 128,
-                      U.row0 + b * p.box, pol_x);
           sp.next(NST);
           ++issued;
         }
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     // ------------------------------------------------------------ epilogue
     // Two warps per lane quarter take alternate 16-row blocks of a unit.  A unit's scales are
     // loaded while the unit before it is computed and read out.
-    const int q = warp & 3, hw = (warp - 2) >> 2, ch = q * 32 + lane;
+    const int q = warp & 3, hw = (warp - kI8EpiWarp0) >> 2, ch = q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
@@ -612,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     prefetch_tmap(&tm_x);
     prefetch_tmap(&tm_w);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 2);  // both producers
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -633,14 +636,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (of this CTA's half)
+  if (warp == 0 || warp == kI8XWarp) {
+    // ------------------------------------------------------------ producers (of this CTA's half)
     if (lane == 0) {
+      const bool x = warp == kI8XWarp;
       const uint64_t pol = policy_evict_last();
       const uint32_t full0 = mapa_shared(bar_full, 0);
       RingPos sp;
       int issued = 0;
-      bool ok = true, waited = false;
+      bool ok = true;
+      if (x) griddep_wait();  // the codes of x come from the preceding grid
       for (int u = pid; u < p.units && ok; u += pairs) {
         const I8Unit<1> U = i8_unit<1>(p, nullptr, u);
         const int64_t t = 2 * (int64_t)U.t + rank;
@@ -651,15 +656,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
             ok = false;
             break;
           }
-          const uint32_t st = sbase + (uint32_t)(sp.slot * kI8PairStage);
-          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * sp.slot, 2 * kI8PairStage);
-          // (a tile past the matrix reads zeros)
-          tma_load_2d_pair(st, &tm_w, full0 + 8u * sp.slot, 0, (int)((t * p.chunks + c) * kTileRows), pol);
-          if (!waited) {
-            griddep_wait();  // the codes of x come from the preceding grid
-            waited = true;
-          }
-          tma_load_2d_pair(st + kWCodeBytes, &tm_x, full0 + 8u * sp.slot, c * 128, U.row0 + (int)rank * half, pol);
+          const uint32_t st = sbase + (uint32_t)(sp.slot * kI8PairStage), fb = full0 + 8u * (uint32_t)sp.slot;
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * sp.slot, kI8PairStage);  // both halves
+          if (x)
+            tma_load_2d_pair(st + kWCodeBytes, &tm_x, fb, c * 128, U.row0 + (int)rank * half, pol);
+          else  // (a tile past the matrix reads zeros)
+            tma_load_2d_pair(st, &tm_w, fb, 0, (int)((t * p.chunks + c) * kTileRows), pol);
           sp.next(NST);
           ++issued;
         }
@@ -714,7 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (of this CTA's channels)
-    const int q = warp & 3, hw = (warp - 2) >> 2, ch = (int)rank * kTileRows + q * 32 + lane;
+    const int q = warp & 3, hw = (warp - kI8EpiWarp0) >> 2, ch = (int)rank * kTileRows + q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     const uint32_t free0 = mapa_shared(bar_acc_free, 0);
     griddep_wait();  // the scales of x come from the preceding grid
