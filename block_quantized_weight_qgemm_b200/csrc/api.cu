@@ -1211,8 +1211,9 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
   if (st != QGEMM_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  i8_plan(N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, routed, &p);
-  if (!routed && p.units == 0) return QGEMM_ERR_SHAPE;  // more than 2^30 units
+  i8_plan(M, N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, p.E, &p);
+  if (routed ? (M / p.NB + std::min<int64_t>(p.E, M)) * p.tiles > 0x3FFFFFFF : p.units == 0)
+    return QGEMM_ERR_SHAPE;  // more than 2^30 units
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;

@@ -23,10 +23,10 @@ namespace qg {
 // ---------------------------------------------------------------------------------------
 constexpr float kI8Inv = 1.f / 127.f;
 constexpr int kI8QuantThreads = 1024;  // at most
-constexpr int kI8QuantRegs = 4;        // 8-element words per thread kept in registers
 
 struct I8QuantParams {
   const uint16_t* x;  // bf16 [M][K]
+  int64_t M;
   int K;
   int8_t* codes;  // [M][K]
   float* scales;  // [M]
@@ -65,9 +65,14 @@ __device__ __forceinline__ uint2 i8_codes8(const uint4& v, float up, float inv, 
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
-// Per row: the largest |x| as bf16 bits (which order like the magnitudes, infinities and NaN
-// above every finite value), the scale, the codes.
-__global__ void __launch_bounds__(kI8QuantThreads) qgemm_i8_quant_kernel(const I8QuantParams p) {
+// Per row: the largest |x| as bf16 bits (which order like the magnitudes, infinities and NaN above
+// every finite value), the scale, the codes.  A row is one warp's (WARP: short rows, eight to a
+// block) or a block's, each thread with up to R words of eight elements in registers; what is left of a
+// long row is read twice.
+// Bound by memory: 2048 x 5120 in 7.7 us (31 MB; a launch's latency and one wave of blocks), 8192 x
+// 5120 in 23 us (5.4 TB/s).
+template <int R, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : kI8QuantThreads) qgemm_i8_quant_kernel(const I8QuantParams p) {
   // The GEMM that follows starts its set-up and its weight copies before it waits for this grid.  A
   // plain one reads nothing else by then, and may launch at once (weights come from a grid that has
   // ended, as the header says); a routed one also reads offsets and tables, which the grid before
@@ -75,43 +80,47 @@ __global__ void __launch_bounds__(kI8QuantThreads) qgemm_i8_quant_kernel(const I
   if (p.early) griddep_launch_dependents();
   griddep_wait();
   if (!p.early) griddep_launch_dependents();
-  const int64_t m = blockIdx.x;
-  const int step = blockDim.x * 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t m = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+  if (WARP && m >= p.M) return;
+  const int k0 = (WARP ? lane : (int)threadIdx.x) * 8, step = WARP ? 256 : (int)blockDim.x * 8;
   const uint16_t* xr = p.x + m * p.K;
-  __shared__ uint32_t red[kI8QuantThreads / 32];
-  uint4 v[kI8QuantRegs];
+  uint4 v[R];
   uint32_t top = 0;  // two maxima of 16 bits
   auto take = [&](const uint4& a) {
     top = __vmaxu2(top, __vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu));
     top = __vmaxu2(top, __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
   };
 #pragma unroll
-  for (int j = 0; j < kI8QuantRegs; ++j) {
-    const int k = threadIdx.x * 8 + j * step;
+  for (int j = 0; j < R; ++j) {
+    const int k = k0 + j * step;
     v[j] = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int j = 0; j < kI8QuantRegs; ++j) take(v[j]);
-  for (int k = threadIdx.x * 8 + kI8QuantRegs * step; k < p.K; k += step)
-    take(*reinterpret_cast<const uint4*>(xr + k));
-  const uint32_t mx = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const uint32_t bits = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? red[lane] : 0u);
+  for (int j = 0; j < R; ++j) take(v[j]);
+  if (!WARP)
+    for (int k = k0 + R * step; k < p.K; k += step) take(*reinterpret_cast<const uint4*>(xr + k));
+  uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+  if (!WARP) {
+    __shared__ uint32_t red[kI8QuantThreads / 32];
+    if (lane == 0) red[threadIdx.x >> 5] = bits;
+    __syncthreads();
+    bits = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? red[lane] : 0u);
+  }
   const bool finite = bits < 0x7F80u;
   const float amax = __uint_as_float(bits << 16);
   const float scale = finite ? __fmul_rn(amax, kI8Inv) : __int_as_float(0x7FC00000);
-  if (threadIdx.x == 0) p.scales[m] = scale;
+  if (k0 == 0) p.scales[m] = scale;
   int8_t* cr = p.codes + m * p.K;
   auto write = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < kI8QuantRegs; ++j) {
-      const int k = threadIdx.x * 8 + j * step;
+    for (int j = 0; j < R; ++j) {
+      const int k = k0 + j * step;
       if (k < p.K) *reinterpret_cast<uint2*>(cr + k) = f(v[j]);
     }
-    for (int k = threadIdx.x * 8 + kI8QuantRegs * step; k < p.K; k += step)
-      *reinterpret_cast<uint2*>(cr + k) = f(*reinterpret_cast<const uint4*>(xr + k));
+    if (!WARP)
+      for (int k = k0 + R * step; k < p.K; k += step)
+        *reinterpret_cast<uint2*>(cr + k) = f(*reinterpret_cast<const uint4*>(xr + k));
   };
   if (!finite || bits == 0) {
     write([](const uint4&) { return make_uint2(0u, 0u); });
@@ -295,14 +304,51 @@ struct I8Scales {
   }
 };
 
+// A unit that a cluster of cs CTAs splits over K (one unit per cluster): 16-row block b is summed and
+// written by rank b % cs.  The others send it their sums through distributed shared memory, into the ring
+// of its stages, which is free by then: [source][own block][matrix][16 rows / 4][128 channels][4 rows].
+constexpr uint32_t kI8Block = 16 * kTileRows * 4;
+
+template <int NMAT>
+__device__ __forceinline__ uint32_t i8_block_at(int rows, int cs, int source, int b, int m) {
+  const int own = ((rows + 15) / 16 + cs - 1) / cs;  // blocks a rank owns at most
+  return (uint32_t)((source * own + b / cs) * NMAT + m) * kI8Block;
+}
+
+template <int NMAT>
+__device__ __forceinline__ void i8_send(const I8Params& p, const I8Unit<NMAT>& V, uint32_t d, int hw, int ch,
+                                        uint32_t ring, int rank) {
+  for (int cb = hw * 16; cb < V.rows; cb += 32) {
+    const int owner = (cb >> 4) % p.cs;
+    if (owner == rank) continue;
+    uint32_t v[NMAT][16];
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) i8_tmem_ld16(d + (uint32_t)(m * p.NB + cb), v[m]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) {
+      const uint32_t at = mapa_shared(
+          ring + i8_block_at<NMAT>(V.rows, p.cs, rank < owner ? rank : rank - 1, cb >> 4, m) + (uint32_t)ch * 16,
+          (uint32_t)owner);
+#pragma unroll
+      for (int r = 0; r < 16; r += 4)
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (uint32_t)(r / 4) * kTileRows * 16),
+                     "r"(v[m][r]), "r"(v[m][r + 1]), "r"(v[m][r + 2]), "r"(v[m][r + 3])
+                     : "memory");
+    }
+  }
+}
+
 // The read-out of one warp's part of a unit's accumulators (d: its lane quarter's first column).
-// ch: the lane's channel within the unit, of `width`.
+// ch: the lane's channel within the unit, of `width`; ring: where a cluster's other CTAs have sent their
+// sums for this rank's blocks (cs above 1).
 template <int NMAT>
 __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT>& V, uint32_t d, int hw, int64_t n,
                                             int ch, int width, const float (&sw)[NMAT],
-                                            const float (&sxl)[kI8Strip / 32]) {
+                                            const float (&sxl)[kI8Strip / 32], const uint8_t* ring, int rank) {
   const bool in = n < p.N;
   for (int cb = hw * 16; cb < V.rows; cb += 32) {
+    if (p.cs > 1 && (cb >> 4) % p.cs != rank) continue;
     __syncwarp();
     uint32_t v[NMAT][16];
 #pragma unroll
@@ -314,6 +360,16 @@ __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT
 #pragma unroll
     for (int r = 0; r < 16; ++r) sx[r] = __shfl_sync(0xffffffffu, sxb, ((b & 1) << 4) + r);
     tmem_ld_wait();
+    for (int o = 0; o < p.cs - 1; ++o)
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        const uint8_t* at = ring + i8_block_at<NMAT>(V.rows, p.cs, o, cb >> 4, m) + ch * 16;
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+          const uint4 a = *reinterpret_cast<const uint4*>(at + (r / 4) * kTileRows * 16);
+          v[m][r] += a.x, v[m][r + 1] += a.y, v[m][r + 2] += a.z, v[m][r + 3] += a.w;
+        }
+      }
     const int nr = min(16, V.rows - cb);
     // 16 rows of one channel: a full block without a branch per row, so that its stores follow one
     // another
@@ -365,6 +421,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   I8Unit<NMAT>* list = reinterpret_cast<I8Unit<NMAT>*>(ctl + 4);
   int* pre = reinterpret_cast<int*>(list + kI8List);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the CTA's (or its cluster's) place among the units
+  const int rank = p.cs > 1 ? (int)cluster_ctarank() : 0;
+  const int first = (int)blockIdx.x / p.cs, stride = (int)gridDim.x / p.cs;
 
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_x);
@@ -423,7 +482,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     __syncthreads();
     // every thread finds one unit of this CTA, so that the roles below read it in one step
     for (int i = threadIdx.x; i < kI8List; i += kI8Threads) {
-      const int64_t u = (int64_t)blockIdx.x + (int64_t)i * gridDim.x;
+      const int64_t u = (int64_t)first + (int64_t)i * stride;
       if (u < units) list[i] = i8_unit<NMAT>(p, pre, (int)u);
     }
   }
@@ -432,7 +491,18 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
   const int set = NMAT * p.NB;  // columns of one accumulator set
-  auto unit = [&](int i, int u) { return p.off && i < kI8List ? list[i] : i8_unit<NMAT>(p, pre, u); };
+  auto unit = [&](int i, int u) {
+    I8Unit<NMAT> U = p.off && i < kI8List ? list[i] : i8_unit<NMAT>(p, pre, u);
+    if (p.cs > 1) {
+      U.c0 = (int)((int64_t)rank * p.chunks / p.cs);
+      U.c1 = (int)((int64_t)(rank + 1) * p.chunks / p.cs);
+    }
+    return U;
+  };
+  I8Unit<NMAT> V;  // (epilogue) the unit at hand
+  I8Scales<NMAT> vs;
+  bool held = false;  // (epilogue, clusters) its accumulators are complete and not read out yet
+  const int q = warp & 3, hw = (warp - kI8EpiWarp0) >> 2, ch = q * 32 + lane;
 
   if (warp == 0 || warp == kI8XWarp) {
     // ------------------------------------------------------------ producers: weights, rows of x
@@ -443,7 +513,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       int issued = 0, i = 0;
       bool ok = true;
       if (x) griddep_wait();  // the codes of x come from the preceding grid
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
+      for (int u = first; u < units && ok; u += stride, ++i) {
         const I8Unit<NMAT> U = unit(i, u);
         const int boxes = (U.rows + p.box - 1) / p.box;
         const uint32_t bytes = x ? (uint32_t)(boxes * p.box * 128) : (uint32_t)(NMAT * kWCodeBytes);
@@ -490,7 +560,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       RingPos sp;
       bool ok = true;
       int i = 0;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++i) {
+      for (int u = first; u < units && ok; u += stride, ++i) {
         const I8Unit<NMAT> U = unit(i, u);
         const uint32_t idesc = i8_idesc(128, (U.rows + 15) & ~15);
         const uint32_t d = tmem + (uint32_t)((i & 1) * set);
@@ -535,7 +605,6 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     // ------------------------------------------------------------ epilogue
     // Two warps per lane quarter take alternate 16-row blocks of a unit.  A unit's scales are
     // loaded while the unit before it is computed and read out.
-    const int q = warp & 3, hw = (warp - kI8EpiWarp0) >> 2, ch = q * 32 + lane;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
@@ -545,22 +614,37 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       U = unit(i, u);
       sc.fetch(p, U, (int64_t)U.t * kTileRows + ch, hw, lane);
     };
-    if (blockIdx.x < units) fetch(0, blockIdx.x);
+    if (first < units) fetch(0, first);
     int i = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
-      const I8Unit<NMAT> V = U;
-      const I8Scales<NMAT> vs = sc;
-      if (u + (int)gridDim.x < units) fetch(i + 1, u + gridDim.x);
+    for (int u = first; u < units; u += stride, ++i) {
+      V = U;
+      vs = sc;
+      if (u + stride < units) fetch(i + 1, u + stride);
       bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
+      if (p.cs > 1) {
+        held = true;
+        break;
+      }
       i8_read_out<NMAT>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw, (int64_t)V.t * kTileRows + ch, ch,
-                        kTileRows, vs.sw, vs.sx);
+                        kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
     }
+  }
+
+  // ------------------------------------------------------------ sum over the cluster
+  if (p.cs > 1) {
+    // every CTA has all its sums: the rings hold nothing any more
+    cluster_sync_all();
+    const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
+    if (held) i8_send<NMAT>(p, V, d, hw, ch, sbase, rank);
+    cluster_sync_all();
+    if (held)
+      i8_read_out<NMAT>(p, V, d, hw, (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, smem, rank);
   }
 
   // ------------------------------------------------------------ teardown
@@ -738,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       if (!ok) break;
       tc_fence_after();
       i8_read_out<1>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
-                     2 * kTileRows, vs.sw, vs.sx);
+                     2 * kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -823,12 +907,25 @@ cudaError_t launch_i8_pack(const float* W, int64_t N, int64_t K, uint8_t* codes,
 
 cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* codes, float* scales, bool early,
                             cudaStream_t stream) {
-  I8QuantParams p{x, (int)K, codes, scales, early ? 1 : 0};
-  // few rows: a thread per word, for the shortest way through a row; many: four words per thread (2048 x
-  // 5120: 14.4, 9.6, 7.6, 10.3 us with 1, 2, 4, 8)
-  const int64_t words = K / 8, per = M <= 2 * kI8SMs ? 1 : kI8QuantRegs;
-  const int threads = (int)std::min<int64_t>(kI8QuantThreads, ((words + per - 1) / per + 31) / 32 * 32);
-  return launch_dep(qgemm_i8_quant_kernel, dim3((unsigned)M), dim3(threads), 0, stream, p);
+  const I8QuantParams p{x, M, (int)K, codes, scales, early ? 1 : 0};
+  const int64_t words = K / 8;
+  const auto warps = [&](auto kern) {
+    return launch_dep(kern, dim3((unsigned)((M + 7) / 8)), dim3(256), 0, stream, p);
+  };
+  const auto block = [&](auto kern, int per) {
+    const int threads = (int)std::min<int64_t>(kI8QuantThreads, ((words + per - 1) / per + 31) / 32 * 32);
+    return launch_dep(kern, dim3((unsigned)M), dim3(threads), 0, stream, p);
+  };
+  // few rows: a thread per word, for the shortest way through a row.  Many: four words per thread (2048 x
+  // 5120: 14.4, 9.6, 7.6, 10.3 us with 1, 2, 4, 8), and of rows that one warp holds in
+  // eight words a lane, eight to a block (81920 x 512: 86 us by blocks, 24 by warps; 16 or 20 words a lane
+  // ran 20 % slower than blocks)
+  if (M <= 2 * kI8SMs) return block(qgemm_i8_quant_kernel<4, false>, 1);
+  if (words <= 32) return warps(qgemm_i8_quant_kernel<1, true>);
+  if (words <= 64) return warps(qgemm_i8_quant_kernel<2, true>);
+  if (words <= 128) return warps(qgemm_i8_quant_kernel<4, true>);
+  if (words <= 256) return warps(qgemm_i8_quant_kernel<8, true>);
+  return block(qgemm_i8_quant_kernel<4, false>, 4);
 }
 
 
@@ -842,15 +939,20 @@ static int sm_count(int dev) {
   return v;
 }
 
-// Tiling of a call: rows is M, or the most rows an expert has.
-//
 // A plain call's tiles go out in full rounds over the SMs (or pairs), each tile over all of K; the tiles
 // of the last round, if they leave SMs idle, are split over K so that their ranges fill it.  A split
 // costs the partials' way through L2 and the reduction's launch, about the time of kI8SplitChunks
 // chunks, so it has to save more than those.
-constexpr int kI8SplitChunks = 8;
+//
+// Where all units fit on the device as clusters of several CTAs, a cluster splits each unit over K and sums
+// in distributed shared memory instead, without a second kernel, at the price of two cluster barriers.
+constexpr int kI8SplitChunks = 8, kI8ClusterChunks = 8;
+// clusters of 0 .. 8 CTAs, one per SM, that a B200 holds at once (by its occupancy calculator)
+constexpr int kI8Clusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 
-void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params* p) {
+// Tiling of a call: rows is M, or (E experts) the most rows an expert has.
+void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p) {
+  const bool routed = E > 0;
   p->pair = !routed && rows > 256;
   p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
   p->chunks = (int)k_chunks(FMT_FP8, K);
@@ -859,13 +961,19 @@ void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params
   // routed: small boxes, so that an expert's rows bring few of its neighbours' with them
   p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, 32) : p->NB;
   p->b_tiles = (int)((rows + p->NB - 1) / p->NB);
-  p->S = 1;
+  p->S = p->cs = 1;
   p->full = p->units = 0;
+  const int64_t all = (int64_t)p->tiles * p->b_tiles;
+  if (!p->pair) {
+    const int64_t most = routed ? all * std::min<int64_t>(E, M) : all;
+    for (int cs = 2; cs <= 8 && cs <= p->chunks; ++cs)
+      if (most <= kI8Clusters[cs] && p->chunks - (p->chunks + cs - 1) / cs > kI8ClusterChunks) p->cs = cs;
+  }
   if (!routed) {
-    const int64_t all = (int64_t)p->tiles * p->b_tiles, slots = p->pair ? kI8SMs / 2 : kI8SMs;
+    const int64_t slots = p->pair ? kI8SMs / 2 : kI8SMs;
     const int64_t rest = all % slots;
     const int64_t S = rest ? std::min<int64_t>(slots / rest, p->chunks) : 1;
-    if (S > 1 && p->chunks - (p->chunks + S - 1) / S > kI8SplitChunks) p->S = (int)S;
+    if (S > 1 && p->cs == 1 && p->chunks - (p->chunks + S - 1) / S > kI8SplitChunks) p->S = (int)S;
     if (all <= 0x3FFFFFFF) {
       p->full = (int)(p->S > 1 ? all - rest : all);
       p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
@@ -880,7 +988,7 @@ void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params
 
 size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M) {
   I8Params p{};
-  i8_plan(N, K, M, 1, false, &p);
+  i8_plan(M, N, K, M, 1, 0, &p);
   return (size_t)(p.units - p.full) * (size_t)p.NB * (p.pair ? 2 : 1) * kTileRows * 4;
 }
 
@@ -894,17 +1002,21 @@ static cudaError_t raise_smem(const void* kern, std::atomic<uint64_t>& set_mask,
 }
 
 template <typename... P, typename... A>
-static cudaError_t launch_gemm(void (*kern)(P...), size_t smem, int grid, cudaStream_t stream, const A&... args) {
+static cudaError_t launch_gemm(void (*kern)(P...), size_t smem, int grid, int cluster, cudaStream_t stream,
+                               const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(kI8Threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;  // (the pair kernel has its cluster size from its declaration)
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
@@ -915,14 +1027,14 @@ static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, 
   if (e != cudaSuccess) return e;
   const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 +
                       (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : 0);
-  // (a ring of half the shared memory, which lets the next product's CTAs in beside these, measured 4 to
-  // 8 % slower)
+  // (a ring of half the shared memory, which lets the next product's CTAs in beside these, measured 3 to
+  // 15 % slower: with memory busy, a chunk takes microseconds to arrive)
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
   // routed: an upper bound, the kernel counts the units that have rows
   const int64_t most = p.off ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M) : p.units;
-  const int grid = (int)std::min<int64_t>(most, sm_count(dev));
-  return launch_gemm(qgemm_i8_kernel<NMAT>, misc + (size_t)p.stages * p.stage_bytes, grid, stream, p, map);
+  const int grid = p.cs > 1 ? (int)most * p.cs : (int)std::min<int64_t>(most, sm_count(dev));
+  return launch_gemm(qgemm_i8_kernel<NMAT>, misc + (size_t)p.stages * p.stage_bytes, grid, p.cs, stream, p, map);
 }
 
 // p: planned (i8_plan), operands filled in; map_x: x's codes in boxes of 128 x p.box; map_w (pair):
@@ -937,7 +1049,7 @@ cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorM
     if (e != cudaSuccess) return e;
     const size_t smem = 1024 + kI8PairStages * kI8PairStage + 8 * (2 * kI8PairStages + 6) + 16;
     const int grid = 2 * std::min(p.units, sm_count(dev) / 2);
-    e = launch_gemm(qgemm_i8_pair_kernel, smem, grid, stream, p, map_x, map_w);
+    e = launch_gemm(qgemm_i8_pair_kernel, smem, grid, 1, stream, p, map_x, map_w);
   } else {
     e = p.nmat == 2 ? launch_i8_impl<2>(p, map_x, dev, stream) : launch_i8_impl<1>(p, map_x, dev, stream);
   }

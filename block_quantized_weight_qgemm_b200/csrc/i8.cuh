@@ -33,12 +33,13 @@ struct I8Params {
   int b_tiles;      // row tiles of a plain call (routed: of an expert, at most)
   int units, full;  // plain: units; the first `full` take all of K, those after write partials
   int S;            // K ranges of a split tile
+  int cs;           // CTAs of a cluster that share a unit's K (then one unit per cluster)
   int stages, stage_bytes, tmem_cols;
   int w_again;      // a weight tile is read by more than one unit
   int* ws;          // partials [units - full][NB][channels of a tile]
 };
 
-void i8_plan(int64_t N, int64_t K, int64_t rows, int nmat, bool routed, I8Params* p);
+void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p);
 size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M);
 cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorMap& map_w, cudaStream_t stream);
 

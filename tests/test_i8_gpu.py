@@ -90,7 +90,7 @@ def test_ties_go_to_even():
     assert torch.equal(codes.cpu()[:, :254].double(), torch.round(n + 0.5)[None].repeat(3, 1))
 
 
-@pytest.mark.parametrize("M,K", [(1, 16), (3, 32), (1, 17408), (5, 8208), (2, 131072), (300, 144)])
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 32), (401, 16), (777, 256), (300, 272), (1001, 512), (600, 1024), (500, 2048), (401, 2064), (1, 17408), (5, 8208), (2, 131072), (300, 144)])
 def test_quant_rows(M, K):
     x = inputs.activations(M, K, seed=M + K)
     codes, scales = qgemm.i8_quant_x(x.cuda())
@@ -416,3 +416,53 @@ def test_captured_gemm_shares_no_state_between_graphs():
         torch.cuda.synchronize()
         for h, y in zip(hs, outs):
             check(y, *quantise(h), p, sw)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 129, 256])
+@pytest.mark.parametrize("N,K", [(100, 1280), (640, 1664), (1300, 2048), (2800, 1024), (5000, 1152), (5700, 1792),
+                                 (9400, 896), (9500, 1536)])
+def test_k_split_over_clusters_and_not(M, N, K):
+    # from 1 to 75 channel tiles: clusters of eight CTAs down to one share a tile's K, in uneven runs
+    g = torch.Generator(device="cuda").manual_seed(N + M)
+    rm = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sw = torch.rand(N, device="cuda", generator=g) + 0.5
+    x = inputs.activations(M, K, seed=M)
+    q, sx = quantise(x)
+    y = qgemm.i8_run(x.cuda(), qgemm.i8_repack_rowmajor(rm, sw))
+    check(y, q, sx, rm.cpu().double(), sw.cpu())
+
+
+@pytest.mark.parametrize("M,N,K", [(1000, 20000, 512), (257, 9600, 2048), (600, 1000, 8192), (64, 19000, 2048)])
+def test_last_round_split_over_k(M, N, K):
+    # full rounds of tiles, then a last round whose tiles are split over K and summed afterwards
+    g = torch.Generator(device="cuda").manual_seed(N + M)
+    rm = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sw = torch.rand(N, device="cuda", generator=g) + 0.5
+    x = inputs.activations(M, K, seed=M)
+    y = qgemm.i8_run(x.cuda(), qgemm.i8_repack_rowmajor(rm, sw))
+    q, sx = quantise(x)
+    check(y, q, sx, rm.cpu().double(), sw.cpu())
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 2), (1, 6, 64), (2, 4, 300), (7, 3, 5)])
+def test_few_routed_rows(T, k, E):
+    # a unit per expert and tile at most, each shared by a cluster
+    g = torch.Generator().manual_seed(T)
+    Nf, Kf = 256, 1040
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    x = inputs.activations(T, Kf, seed=k)
+    xs, off, _ = qgemm.moe_dispatch(x.cuda(), ids.cuda(), E)
+    Ws = [inputs.weights(Nf, Kf, seed=i) for i in range(4)]
+    packed, refs = [qgemm.i8_pack(W.cuda()) for W in Ws], [quantise(W) for W in Ws]
+    gate = qgemm.I8ExpertTable([packed[e % 4] for e in range(E)])
+    up = qgemm.I8ExpertTable([packed[(e + 1) % 4] for e in range(E)])
+    o = off.tolist()
+    mr = max(b - a for a, b in zip(o, o[1:]))
+    y = qgemm.i8_moe_run(xs, off, gate, mr)
+    h = qgemm.i8_moe_gate_up(xs, off, gate, up, mr)
+    for e in range(E):
+        if o[e] < o[e + 1]:
+            q, sx = quantise(xs[o[e]:o[e + 1]].cpu())
+            check(y[o[e]:o[e + 1]], q, sx, *refs[e % 4])
+            gg, uu = [(q @ p.t()) * s.double() * sx.double()[:, None] for p, s in (refs[e % 4], refs[(e + 1) % 4])]
+            h_check(h[o[e]:o[e + 1]], gg, uu)
