@@ -381,10 +381,10 @@ struct Vec<__nv_bfloat16, N> {
 };
 
 // y[t] = sum_j w[t][j] ys[row[t][j]], j ascending (w absent: 1); a row outside [0, S) is none.
-// The loads of `per` slots (at most B) go together: k in equal batches.
+// The loads of B slots go together.
 template <typename TI, typename TO, int N, int B>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI* __restrict__ ys, int64_t T,
-                                                                        int H, int k, int per, int64_t S,
+                                                                        int H, int k, int64_t S,
                                                                         const int* __restrict__ row,
                                                                         const float* __restrict__ w,
                                                                         TO* __restrict__ y) {
@@ -398,14 +398,13 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < k; j0 += per) {
+    for (int j0 = 0; j0 < k; j0 += B) {
       typename Vec<TI, N>::R raw[B];
       float wj[B];
       bool has[B];
 #pragma unroll
       for (int j = 0; j < B; ++j) {
-        const bool in = j < per && j0 + j < k;
-        const int ro = in ? __ldg(r + j0 + j) : -1;
+        const int ro = j0 + j < k ? __ldg(r + j0 + j) : -1;
         has[j] = ro >= 0 && ro < S;
         wj[j] = has[j] && wt ? __ldg(wt + j0 + j) : 1.f;
         raw[j].clear();
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI
 
 // dys[row] = w dy and dw = <dy, ys[row]>: a warp per slot (the k warps of a token find its dy in L1).
 // A lane sums its elements in ascending order, the lanes are added in a fixed tree.
-constexpr int kGradSteps = 4;  // steps of a row loaded together
+constexpr int kGradSteps = 2;  // steps of a row loaded together (34, 30, 34, 33 us with 1, 2, 4, 8: 2048 tokens, bf16)
 
 template <typename TD, typename TY, int N>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_grad_kernel(
@@ -554,7 +553,7 @@ static cudaError_t combine_batch(const void* ys, int64_t T, int64_t H, int k, co
   const int64_t pieces = (H / N + s.bx - 1) / s.bx;
   const unsigned gy = (unsigned)(blocks < 2 * kSMs ? std::min<int64_t>(pieces, 64) : 1);
   return launch_dep(qgemm_moe_combine_kernel<TI, TO, N, B>, dim3((unsigned)blocks, gy), dim3(s.bx, s.by), 0, stream,
-                    static_cast<const TI*>(ys), T, (int)H, k, batch_of(k, B), T * k, row, w, static_cast<TO*>(y));
+                    static_cast<const TI*>(ys), T, (int)H, k, T * k, row, w, static_cast<TO*>(y));
 }
 
 template <typename TI, typename TO>
@@ -562,10 +561,25 @@ static cudaError_t combine_impl(const void* ys, int64_t T, int64_t H, int k, con
                                 void* y, cudaStream_t stream) {
   return by_width(H, [&](auto n) {
     constexpr int N = decltype(n)::value;
-    // registers for no more slots than a batch has: two slots in the registers of eight ran 35 % slower
-    if (k <= 2) return combine_batch<TI, TO, N, 2>(ys, T, H, k, row, w, y, stream);
-    if (k <= 4 || (N == 8 && sizeof(TI) == 4)) return combine_batch<TI, TO, N, 4>(ys, T, H, k, row, w, y, stream);
-    return combine_batch<TI, TO, N, 8>(ys, T, H, k, row, w, y, stream);
+    const auto go = [&](auto b) {
+      return combine_batch<TI, TO, N, decltype(b)::value>(ys, T, H, k, row, w, y, stream);
+    };
+    // A batch's loop has exactly its slots: ten slots as two batches of five took 16.5 us (2048 tokens, bf16)
+    // where loops of eight, five of them used, took 19, and two slots in a loop of eight 66 where 40
+    // suffice.  At most eight slots, or five of 32-byte pieces (registers).
+    if constexpr (N == 8) {
+      const int b = batch_of(k, sizeof(TI) == 2 ? 8 : 5);
+      if (b == 1) return go(std::integral_constant<int, 1>{});
+      if (b == 2) return go(std::integral_constant<int, 2>{});
+      if (b == 3) return go(std::integral_constant<int, 3>{});
+      if (b == 5) return go(std::integral_constant<int, 5>{});
+      if constexpr (sizeof(TI) == 2) {
+        if (b == 6) return go(std::integral_constant<int, 6>{});
+        if (b == 7) return go(std::integral_constant<int, 7>{});
+        if (b == 8) return go(std::integral_constant<int, 8>{});
+      }
+    }
+    return go(std::integral_constant<int, 4>{});
   });
 }
 
