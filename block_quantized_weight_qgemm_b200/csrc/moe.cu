@@ -41,14 +41,15 @@ static cudaError_t launch_dep(void (*kern)(P...), dim3 grid, dim3 block, size_t 
 // ---------------------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------------------
-constexpr int kSmallSlots = 4096;  // up to here one launch dispatches (its work grows with the square)
+constexpr int kSmallSlots = 8192;  // one launch can dispatch up to here
 constexpr int kSmallThreads = 256;
 constexpr int kSortCtas = 8;       // a portable cluster
-constexpr int kSortMaxWarps = 16;
-constexpr int kIdLoads = 8;        // expert ids loaded together
+constexpr int kIdLoads = 8;        // expert ids a lane of the sort loads together
+constexpr int kSmallLoads = 4;     // and a thread of the small dispatch
 
-// Exclusive prefix sum of v over the block's threads (whole warps, at most kSortMaxWarps), in thread
-// order; *total gets the sum.  red: an int per warp.
+// Exclusive prefix sum of v over the threads of a block of W warps, in thread order; *total gets the sum.
+// red: an int per warp.
+template <int W>
 __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int inc = v;
@@ -60,7 +61,8 @@ __device__ __forceinline__ int block_excl_scan(int v, int* red, int* total) {
   if (lane == 31) red[w] = inc;
   __syncthreads();
   int base = 0, sum = 0;
-  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
     if (i < w) base += red[i];
     sum += red[i];
   }
@@ -86,15 +88,15 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
   if ((int)blockIdx.x == T) {
     for (int e = tid; e < E; e += kSmallThreads) sm_hist[e] = 0;
     __syncthreads();
-    for (int i0 = 0; i0 < S; i0 += kIdLoads * kSmallThreads) {
-      int e[kIdLoads];
+    for (int i0 = 0; i0 < S; i0 += kSmallLoads * kSmallThreads) {
+      int e[kSmallLoads];
 #pragma unroll
-      for (int q = 0; q < kIdLoads; ++q) {
+      for (int q = 0; q < kSmallLoads; ++q) {
         const int i = i0 + q * kSmallThreads + tid;
         e[q] = i < S ? __ldg(ids + i) : -1;
       }
 #pragma unroll
-      for (int q = 0; q < kIdLoads; ++q)
+      for (int q = 0; q < kSmallLoads; ++q)
         if ((unsigned)e[q] < (unsigned)E) atomicAdd(&sm_hist[e[q]], 1);
     }
     __syncthreads();
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
     for (int e0 = 0; e0 < E; e0 += kSmallThreads) {
       const int e = e0 + tid;
       int sum;
-      const int first = carry + block_excl_scan(e < E ? sm_hist[e] : 0, &red[0][0], &sum);
+      const int first = carry + block_excl_scan<kSmallThreads / 32>(e < E ? sm_hist[e] : 0, &red[0][0], &sum);
       carry += sum;
       if (e < E) offsets[e] = first;
     }
@@ -120,15 +122,15 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
       key[j] = (unsigned)e < (unsigned)E ? e * kSmallSlots + (t * k + j0 + j) : -1;
       cnt[j] = 0;
     }
-    for (int i0 = 0; i0 < S; i0 += kIdLoads * kSmallThreads) {
-      int e[kIdLoads];
+    for (int i0 = 0; i0 < S; i0 += kSmallLoads * kSmallThreads) {
+      int e[kSmallLoads];
 #pragma unroll
-      for (int q = 0; q < kIdLoads; ++q) {
+      for (int q = 0; q < kSmallLoads; ++q) {
         const int i = i0 + q * kSmallThreads + tid;
         e[q] = i < S ? __ldg(ids + i) : -1;
       }
 #pragma unroll
-      for (int q = 0; q < kIdLoads; ++q) {
+      for (int q = 0; q < kSmallLoads; ++q) {
         const int ki = (unsigned)e[q] < (unsigned)E ? e[q] * kSmallSlots + i0 + q * kSmallThreads + tid : 0x7FFFFFFF;
 #pragma unroll
         for (int j = 0; j < B; ++j) cnt[j] += ki < key[j] ? 1 : 0;
@@ -162,13 +164,16 @@ __global__ void __launch_bounds__(kSmallThreads) qgemm_moe_dispatch_small_kernel
   }
 }
 
-// Many slots: one cluster of eight CTAs sorts, each a run of S / 8 slots and each warp a run of those.
-// Every warp counts its run's slots per expert; the CTAs exchange their totals through distributed shared
-// memory, so that each knows the first row of every (expert, warp); then each warp walks its run in
-// order, 32 slots at a time: a slot's row is the running row of its expert plus the lanes of the same
-// expert before it.  Shared memory: [warps][E] counts, then running rows; [E] totals of the CTA.
-// (Counts per block in global memory and a second kernel for the rows took 8 us where this takes 5, at
-// 20480 slots of 512 experts.)
+// Many slots: one cluster of eight CTAs sorts, each a run of S / 8 slots and each of its W warps a run of
+// those.  Every warp counts its run's slots per expert, and the counts become, per expert, the slots of
+// the CTA's earlier warps; the CTAs exchange their totals through distributed shared memory, which gives
+// each the first row of every expert's slots in it; then each warp walks its run in order, 32 slots at a
+// time: a slot's row is its expert's first row, plus the slots of that expert in earlier warps, in the
+// warp's earlier slots and in earlier lanes.  Shared memory: [W][E] counts, [E] totals, [E] first rows.
+//
+// Bound by latencies: 20480 slots of 512 experts take about 7 us, two of them the launch.  The lanes of one
+// expert are found by a ballot per bit of its number: __match_any_sync took 1080 cycles per 32 slots of
+// mostly different experts, these 580.
 struct SortParams {
   const int* ids;  // [S]
   int S, E;
@@ -176,47 +181,59 @@ struct SortParams {
   int* row;      // [S]
 };
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortMaxWarps * 32)
-    qgemm_moe_sort_kernel(const SortParams p) {
+// (relaxed: it publishes no writes, and a release would wait for those to global memory)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <int W>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(W * 32) qgemm_moe_sort_kernel(const SortParams p) {
   extern __shared__ int sm_cnt[];
-  __shared__ int red[kSortMaxWarps];
-  const int W = blockDim.x >> 5, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __shared__ int red[W];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, E = p.E;
   const int rank = (int)cluster_ctarank();
-  int* tot = sm_cnt + W * p.E;
-  for (int i = threadIdx.x; i < W * p.E; i += blockDim.x) sm_cnt[i] = 0;
+  int* tot = sm_cnt + W * E;
+  int* base = tot + E;
+  for (int i = threadIdx.x; i < W * E; i += W * 32) sm_cnt[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  __syncthreads();
   const int64_t share = ((int64_t)p.S + kSortCtas * W - 1) / (kSortCtas * W);
   const int s0 = (int)min((int64_t)p.S, share * (rank * W + w)), s1 = (int)min((int64_t)p.S, s0 + share);
-  int* cnt = sm_cnt + w * p.E;
+  int* cnt = sm_cnt + w * E;
+  // an expert outside [0, E) becomes E, which is counted nowhere
   auto load = [&](int s, int (&e)[kIdLoads]) {
 #pragma unroll
     for (int q = 0; q < kIdLoads; ++q) {
-      e[q] = s + 32 * q + lane < s1 ? __ldg(p.ids + s + 32 * q + lane) : -1;
-      if ((unsigned)e[q] >= (unsigned)p.E) e[q] = -1;
+      e[q] = s1 - s > 32 * q + lane ? __ldg(p.ids + s + 32 * q + lane) : E;
+      if ((unsigned)e[q] > (unsigned)E) e[q] = E;
     }
   };
   int id[kIdLoads];
-  for (int s = s0; s < s1; s += 32 * kIdLoads) {
-    load(s, id);
+  if (s0 < s1) load(s0, id);
+  __syncthreads();
+  for (int64_t s = s0; s < s1; s += 32 * kIdLoads) {
+    if (s != s0) load((int)s, id);
 #pragma unroll
     for (int q = 0; q < kIdLoads; ++q)
-      if (id[q] >= 0) atomicAdd(&cnt[id[q]], 1);
+      if (id[q] < E) atomicAdd(&cnt[id[q]], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-    int sum = 0;
+  for (int e = threadIdx.x; e < E; e += W * 32) {
+    int c[W], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kSortMaxWarps; ++i) sum += i < W ? sm_cnt[i * p.E + e] : 0;
+    for (int i = 0; i < W; ++i) c[i] = sm_cnt[i * E + e];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      sm_cnt[i * E + e] = sum;
+      sum += c[i];
+    }
     tot[e] = sum;
   }
   cluster_sync_all();
   int carry = 0;
-  for (int e0 = 0; e0 < p.E; e0 += blockDim.x) {
+  for (int e0 = 0; e0 < E; e0 += W * 32) {
     const int e = e0 + threadIdx.x;
     int all = 0, before = 0;
-    if (e < p.E) {
+    if (e < E) {
       const uint32_t a = smem_u32(tot + e);
       int c[kSortCtas];
 #pragma unroll
@@ -229,37 +246,44 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortMaxWarp
       }
     }
     int sum;
-    const int first = carry + block_excl_scan(all, red, &sum);
+    const int first = carry + block_excl_scan<W>(all, red, &sum);
     carry += sum;
-    if (e < p.E) {
-      int at = first + before, n[kSortMaxWarps];
-#pragma unroll
-      for (int i = 0; i < kSortMaxWarps; ++i) n[i] = i < W ? sm_cnt[i * p.E + e] : 0;
-#pragma unroll
-      for (int i = 0; i < kSortMaxWarps; ++i) {
-        if (i < W) sm_cnt[i * p.E + e] = at;
-        at += n[i];
-      }
+    if (e < E) {
+      base[e] = first + before;
       if (rank == 0) p.offsets[e] = first;
     }
   }
-  if (rank == 0 && threadIdx.x == 0) p.offsets[p.E] = carry;
-  cluster_sync_all();  // (also: no CTA leaves while another reads its totals)
-  for (int s = s0; s < s1; s += 32 * kIdLoads) {
-    load(s, id);
+  cluster_arrive();  // this CTA has read the others' totals
+  if (rank == 0 && threadIdx.x == 0) p.offsets[E] = carry;
+  __syncthreads();
+  const int bits = 32 - __clz(E);  // of 0 .. E
+  for (int64_t s = s0; s < s1; s += 32 * kIdLoads) {
+    if (s1 - s0 > 32 * kIdLoads) load((int)s, id);
+    unsigned same[kIdLoads];  // the lanes of the lane's expert
+#pragma unroll
+    for (int q = 0; q < kIdLoads; ++q) same[q] = 0xffffffffu;
+    const int nq = (int)min((int64_t)kIdLoads, (s1 - s + 31) / 32);
+    for (int b = 0; b < bits; ++b)
+#pragma unroll
+      for (int q = 0; q < kIdLoads; ++q) {
+        if (q >= nq) break;
+        const bool one = (id[q] >> b) & 1;
+        const unsigned m = __ballot_sync(0xffffffffu, one);
+        same[q] &= one ? m : ~m;
+      }
 #pragma unroll
     for (int q = 0; q < kIdLoads; ++q) {
-      if (s + 32 * q >= s1) break;
-      const int e = id[q];
-      const unsigned same = __match_any_sync(0xffffffffu, e);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int base = e >= 0 ? cnt[e] : 0;
+      if (q >= nq) break;
+      const int64_t at = s + 32 * q + lane;
+      const int e = id[q], before = __popc(same[q] & ((1u << lane) - 1u));
+      const int run = e < E ? cnt[e] : 0;
       __syncwarp();
-      if (e >= 0 && before == 0) cnt[e] = base + __popc(same);
+      if (e < E && before == 0) cnt[e] = run + __popc(same[q]);
       __syncwarp();
-      if (s + 32 * q + lane < s1) p.row[s + 32 * q + lane] = e >= 0 ? base + before : -1;
+      if (at < s1) p.row[at] = e < E ? base[e] + run + before : -1;
     }
   }
+  cluster_wait();  // no CTA leaves while another reads its totals
 }
 
 // ---------------------------------------------------------------------------------------
@@ -481,17 +505,31 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_grad_kernel(
 // ---------------------------------------------------------------------------------------
 // Host-side launchers
 // ---------------------------------------------------------------------------------------
-static cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, cudaStream_t stream) {
-  const SortParams p{ids, (int)S, E, offsets, row};
-  // as many warps as have their counts in shared memory (all 16 up to 3400 experts)
-  const int warps = std::min(kSortMaxWarps, (kSmemLimit - 1024) / (4 * E) - 1);
-  const size_t smem = (size_t)(warps + 1) * E * 4;
+template <int W>
+static cudaError_t sort_impl(const SortParams& p, cudaStream_t stream) {
+  const size_t smem = (size_t)(W + 2) * p.E * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(qgemm_moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(qgemm_moe_sort_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemLimit - 1024);
     if (e != cudaSuccess) return e;
   }
-  return launch_dep(qgemm_moe_sort_kernel, dim3(kSortCtas), dim3(warps * 32), smem, stream, p);
+  return launch_dep(qgemm_moe_sort_kernel<W>, dim3(kSortCtas), dim3(W * 32), smem, stream, p);
+}
+
+static cudaError_t launch_moe_sort(const int* ids, int64_t S, int E, int* offsets, int* row, cudaStream_t stream) {
+  const SortParams p{ids, (int)S, E, offsets, row};
+  // as many warps as have their counts in shared memory
+  return (size_t)18 * E * 4 <= kSmemLimit - 1024 ? sort_impl<16>(p, stream) : sort_impl<8>(p, stream);
+}
+
+// Whether one launch dispatches: every token then counts over all slots, 6 instructions per slot and pass and
+// 2 per slot and own slot, about 0.06 us per million beyond the 3 us of a launch.  The sort and the gather
+// after it take 4.5 us for few experts and 7 for 512, so 40 million is the border: 256 tokens top-10 (21
+// million) 4.4 against 7 us; 450 (65 million) 8.5 against 7; 1500 tokens top-2 of 8 (45 million) 4.7
+// against 4.6 us.
+static bool dispatch_small(int64_t T, int k) {
+  const int64_t S = T * k;
+  return S <= kSmallSlots && T * S * (6 * ((k + 7) / 8) + 2 * k) <= 40000000;
 }
 
 // k slots in equal batches of at most b.
@@ -506,7 +544,7 @@ static cudaError_t dispatch_impl(const void* x, int64_t T, int64_t row_bytes, co
   const int nvec = (int)(row_bytes / (int64_t)sizeof(V));
   const V* xv = static_cast<const V*>(x);
   V* xsv = static_cast<V*>(xs);
-  if (T * k <= kSmallSlots) {
+  if (dispatch_small(T, k)) {
     // the slots of a token in equal batches, each counted in one pass over all slots
     auto small = [&](auto b) {
       return launch_dep(qgemm_moe_dispatch_small_kernel<V, decltype(b)::value>, dim3((unsigned)T + 1),

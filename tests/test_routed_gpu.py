@@ -57,7 +57,8 @@ def randn(*shape, dtype=F32, seed=0):
 
 
 SORTS = [(1, 1, 1), (1, 8, 64), (3, 2, 5), (64, 10, 512), (37, 3, 7), (255, 1, 256), (410, 10, 512),
-         (1025, 4, 4), (2048, 10, 512), (700, 7, 4096), (513, 33, 40), (30011, 6, 257)]
+         (1025, 4, 4), (2048, 10, 512), (700, 7, 4096), (513, 33, 40), (30011, 6, 257), (4097, 1, 64),
+         (2000, 1, 3), (1500, 5, 3500), (8191, 2, 511), (50000, 2, 1), (819, 10, 512)]
 
 
 @pytest.mark.parametrize("kind", ["random", "drop", "none", "one"])
