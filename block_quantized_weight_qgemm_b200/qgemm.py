@@ -423,15 +423,17 @@ def _at(stream, *tensors):
     needs, its stream handle).  The library launches on the current device."""
     i = tensors[0].get_device()
     for t in tensors:
-        assert t.get_device() == i >= 0 and t.is_contiguous()
-    here = torch.cuda.current_device()
-    if stream is None:
-        return None if i == here else torch.cuda.device(i), _raw_stream(i)
-    return None if i == here else torch.cuda.device(i), stream.cuda_stream
+        if t.get_device() != i or not t.is_contiguous():
+            raise AssertionError("the tensors of a call are contiguous and on one device")
+    assert i >= 0, "the tensors of a call are on a CUDA device"
+    guard = None if i == _current_device() else torch.cuda.device(i)
+    return guard, _raw_stream(i) if stream is None else stream.cuda_stream
 
 
-def _raw_stream(device_index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device_index)
+# torch's own accessors behind torch.cuda.current_device() and current_stream(), without the stream
+# object (3 us); the device is initialised once a tensor lies on it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _call(name: str, guard, *args):
@@ -443,6 +445,12 @@ def _call(name: str, guard, *args):
             status = fn(*args)
     if status != OK:
         raise QgemmError(status, name)
+
+
+def _row_dtype(t) -> int:
+    d = _ROW_DTYPES.get(t.dtype)
+    assert d is not None, "rows are bf16 or fp32"
+    return d
 
 
 def _scratch(nbytes: int, like, stream):
@@ -463,7 +471,7 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
     T, H = x.shape
     T2, k = experts.shape
-    dt = _ROW_DTYPES[x.dtype]
+    dt = _row_dtype(x)
     assert T2 == T and experts.dtype == torch.int32
     if xs is None:
         xs = x.new_empty((T * k, H))
@@ -504,8 +512,8 @@ def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | 
     T, k, H = _routed(dxs, rows)
     dx = _routed_out(dx, T, H, dx_dtype, dxs)
     guard, st = _at(stream, dxs, rows, dx)
-    _call("qgemm_moe_dispatch_grad", guard, dxs.data_ptr(), _ROW_DTYPES[dxs.dtype], T, H, rows.data_ptr(), k,
-          dx.data_ptr(), _ROW_DTYPES[dx.dtype], st)
+    _call("qgemm_moe_dispatch_grad", guard, dxs.data_ptr(), _row_dtype(dxs), T, H, rows.data_ptr(), k,
+          dx.data_ptr(), _row_dtype(dx), st)
     return dx
 
 
@@ -516,8 +524,8 @@ def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
     assert weights.dtype == torch.float32 and weights.shape == (T, k)
     y = _routed_out(y, T, H, y_dtype, ys)
     guard, st = _at(stream, ys, rows, weights, y)
-    _call("qgemm_moe_combine", guard, ys.data_ptr(), _ROW_DTYPES[ys.dtype], T, H, rows.data_ptr(),
-          weights.data_ptr(), k, y.data_ptr(), _ROW_DTYPES[y.dtype], st)
+    _call("qgemm_moe_combine", guard, ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(),
+          weights.data_ptr(), k, y.data_ptr(), _row_dtype(y), st)
     return y
 
 
@@ -532,8 +540,8 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
     dw = _routed_out(dw, T, k, torch.float32, ys)
     assert dw.dtype == torch.float32
     guard, st = _at(stream, dy, ys, rows, weights, dys, dw)
-    _call("qgemm_moe_combine_grad", guard, dy.data_ptr(), _ROW_DTYPES[dy.dtype], ys.data_ptr(),
-          _ROW_DTYPES[ys.dtype], T, H, rows.data_ptr(), weights.data_ptr(), k, dys.data_ptr(),
+    _call("qgemm_moe_combine_grad", guard, dy.data_ptr(), _row_dtype(dy), ys.data_ptr(),
+          _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k, dys.data_ptr(),
           dw.data_ptr(), st)
     return dys, dw
 
@@ -616,7 +624,7 @@ def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=
         workspace = _scratch(i8_workspace_size(w.N, K, M), x, stream)
     guard, st = _at(stream, x, w.codes, w.scales, y, workspace)
     _call("qgemm_i8_run", guard, x.data_ptr(), M, K, w.codes.data_ptr(), w.scales.data_ptr(), w.N, y.data_ptr(),
-          _ROW_DTYPES[y.dtype], workspace.data_ptr(), _nbytes(workspace), st)
+          _row_dtype(y), workspace.data_ptr(), _nbytes(workspace), st)
     return y
 
 
@@ -656,7 +664,7 @@ def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_r
         workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x, stream)
     guard, st = _at(stream, x, offsets, tab.codes, y, workspace)
     _call("qgemm_i8_moe_run", guard, x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows,
-          tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N, y.data_ptr(), _ROW_DTYPES[y.dtype],
+          tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N, y.data_ptr(), _row_dtype(y),
           workspace.data_ptr(), _nbytes(workspace), st)
     return y
 

@@ -466,3 +466,62 @@ def test_few_routed_rows(T, k, E):
             check(y[o[e]:o[e + 1]], q, sx, *refs[e % 4])
             gg, uu = [(q @ p.t()) * s.double() * sx.double()[:, None] for p, s in (refs[e % 4], refs[(e + 1) % 4])]
             h_check(h[o[e]:o[e + 1]], gg, uu)
+
+
+@pytest.mark.parametrize("T", [40, 2100])
+def test_routings_one_after_another(T):
+    # the products read the offsets early in their launch: with no wait between the steps, every one sees
+    # its own routing (one launch dispatches 40 tokens, two 2100)
+    k, E, H, F, rounds = 4, 16, 256, 128, 12
+    g = torch.Generator().manual_seed(T)
+    tab8 = qgemm.I8ExpertTable([qgemm.i8_pack(inputs.weights(F, H, seed=e).cuda()) for e in range(E)])
+    tab4 = qgemm.ExpertTable([qgemm.pack("nvfp4", inputs.weights(F, H, seed=e).cuda()) for e in range(E)])
+    x = inputs.activations(T, H, seed=1).cuda()
+    w = torch.rand(T, k, generator=g).cuda()
+    like = [torch.rand(E, generator=g).pow(4) for _ in range(rounds)]     # the first experts of each differ
+    ids = [torch.multinomial(p, T * k, replacement=True, generator=g).view(T, k).int().cuda() for p in like]
+
+    def step(i):
+        xs, off, rows = qgemm.moe_dispatch(x, ids[i], E)
+        return (qgemm.moe_combine(qgemm.i8_moe_run(xs, off, tab8, T * k), rows, w, y_dtype=F32),
+                qgemm.moe_combine(qgemm.moe_run(xs, off, tab4, 200), rows, w, y_dtype=F32) if T == 40 else None)
+
+    apart = []
+    for i in range(rounds):
+        apart.append(step(i))
+        torch.cuda.synchronize()
+    together = [step(i) for i in range(rounds)]
+    torch.cuda.synchronize()
+    for a, b in zip(apart, together):
+        assert torch.equal(a[0], b[0]) and (a[1] is None or torch.equal(a[1], b[1]))
+
+
+def test_no_token_has_an_expert():
+    ids = torch.full((5, 3), -1, dtype=torch.int32, device="cuda")
+    x = inputs.activations(5, 256).cuda()
+    xs, off, rows = qgemm.moe_dispatch(x, ids, 4, xs=torch.zeros(15, 256, dtype=BF16, device="cuda"))
+    tab = qgemm.I8ExpertTable([qgemm.i8_pack(inputs.weights(128, 256, seed=e).cuda()) for e in range(4)])
+    y = torch.full((15, 128), 7.0, device="cuda")
+    qgemm.i8_moe_run(xs, off, tab, 15, y=y)
+    h = torch.full((15, 128), 7.0, dtype=BF16, device="cuda")
+    qgemm.i8_moe_gate_up(xs, off, tab, tab, 15, h=h)
+    assert off.tolist() == [0] * 5 and (y == 7).all() and (h == 7).all() and (xs == 0).all()
+    assert (qgemm.moe_combine(y, rows, torch.ones(5, 3, device="cuda")) == 0).all()
+
+
+def test_on_a_stream_of_its_own():
+    # x is made on a side stream and the product runs there; its workspace is the call's own
+    w, p, sw = weight(640, 2048)
+    side = torch.cuda.Stream()
+    xs = [inputs.activations(33, 2048, seed=s) for s in range(6)]
+    pinned = [x.pin_memory() for x in xs]
+    ys = []
+    for h in pinned:
+        with torch.cuda.stream(side):
+            x = h.cuda(non_blocking=True)
+        x.record_stream(side)
+        ys.append(qgemm.i8_run(x, w, stream=side))
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # takes freed blocks, on this stream
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        check(y, *quantise(x), p, sw)
