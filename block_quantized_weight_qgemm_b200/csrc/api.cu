@@ -1184,25 +1184,30 @@ int check_i8(int64_t N, int64_t K) {
   if (st != QGEMM_OK) return st;
   return K > kI8MaxK ? QGEMM_ERR_SHAPE : QGEMM_OK;
 }
-// workspace: the codes and scales of the rows, then a plain call's split-K partials
+// workspace: the codes and scales of the rows, then a plain call's split-K partials; none where the
+// product quantises x itself
 struct I8Ws {
   size_t scales, partials, total;
 };
-I8Ws i8_ws(int64_t N, int64_t K, int64_t M, bool routed) {
+I8Ws i8_ws(const I8Params& p, int64_t M, int64_t K) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-  I8Ws w;
+  I8Ws w{};
+  if (p.fused) return w;
   w.scales = up((size_t)M * (size_t)K);
   w.partials = w.scales + up((size_t)M * 4);
-  w.total = w.partials + (routed ? 0 : up(i8_partial_bytes(N, K, M)));
+  w.total = w.partials + up(i8_partial_bytes(p));
   return w;
 }
 // quantise x, then the GEMM that `p` describes (its x operand and tiling are filled in here)
 int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, void* workspace,
                 size_t workspace_bytes, void* stream) {
   const bool routed = p.off != nullptr;
-  const I8Ws w = i8_ws(N, K, M, routed);
-  if (!workspace || workspace_bytes < w.total) return QGEMM_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return QGEMM_ERR_ALIGN;
+  i8_plan(M, N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, p.E, &p);
+  if (routed ? (M / p.NB + std::min<int64_t>(p.E, M)) * p.tiles > 0x3FFFFFFF : p.units == 0)
+    return QGEMM_ERR_SHAPE;  // more than 2^30 units
+  const I8Ws w = i8_ws(p, M, K);
+  if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return QGEMM_ERR_WORKSPACE;
+  if (workspace && !aligned16(workspace)) return QGEMM_ERR_ALIGN;
   if (!device_ok()) return QGEMM_ERR_DEVICE;
   p.dev_err = error_word();
   if (!p.dev_err) return cuda_fail(cudaGetLastError(), "cudaGetSymbolAddress");
@@ -1211,26 +1216,26 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
   if (st != QGEMM_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
-  i8_plan(M, N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, p.E, &p);
-  if (routed ? (M / p.NB + std::min<int64_t>(p.E, M)) * p.tiles > 0x3FFFFFFF : p.units == 0)
-    return QGEMM_ERR_SHAPE;  // more than 2^30 units
   p.M = (int)M;
   p.N = (int)N;
   p.K = (int)K;
-  p.xcodes = reinterpret_cast<const int8_t*>(wsb);
-  p.xscales = reinterpret_cast<const float*>(wsb + w.scales);
-  p.ws = reinterpret_cast<int*>(wsb + w.partials);
-  CUtensorMap map, map_w{};
-  const int64_t w_rows = row_tiles(N) * p.chunks * kTileRows;  // the codes as rows of 128 bytes
-  if (p.pair && w_rows > 0x7FFFFFFF - 512 * (int64_t)p.chunks) return QGEMM_ERR_SHAPE;
-  if (!i8_map(&map, dev, wsb, M, K, (uint32_t)p.box, true) ||
-      (p.pair && !i8_map(&map_w, dev, p.codes[0], w_rows, 128, 128, false))) {
-    snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled failed");
-    return QGEMM_ERR_CUDA;
+  p.x = static_cast<const uint16_t*>(x);
+  CUtensorMap map{}, map_w{};
+  cudaError_t e = cudaSuccess;
+  if (!p.fused) {
+    p.xcodes = reinterpret_cast<const int8_t*>(wsb);
+    p.xscales = reinterpret_cast<const float*>(wsb + w.scales);
+    p.ws = reinterpret_cast<int*>(wsb + w.partials);
+    const int64_t w_rows = row_tiles(N) * p.chunks * kTileRows;  // the codes as rows of 128 bytes
+    if (p.pair && w_rows > 0x7FFFFFFF - 512 * (int64_t)p.chunks) return QGEMM_ERR_SHAPE;
+    if (!i8_map(&map, dev, wsb, M, K, (uint32_t)p.box, true) ||
+        (p.pair && !i8_map(&map_w, dev, p.codes[0], w_rows, 128, 128, false))) {
+      snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled failed");
+      return QGEMM_ERR_CUDA;
+    }
+    e = launch_i8_quant(p.x, M, K, reinterpret_cast<int8_t*>(wsb), reinterpret_cast<float*>(wsb + w.scales), !routed, s);
+    if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
   }
-  cudaError_t e = launch_i8_quant(static_cast<const uint16_t*>(x), M, K, reinterpret_cast<int8_t*>(wsb),
-                                  reinterpret_cast<float*>(wsb + w.scales), !routed, s);
-  if (e != cudaSuccess) return cuda_fail(e, "int8 quantisation launch");
   if (g_prof_begin) cudaEventRecord(g_prof_begin, s);
   e = launch_i8_gemm(p, map, map_w, s);
   if (e != cudaSuccess) return cuda_fail(e, "int8 gemm launch");
@@ -1296,7 +1301,10 @@ int qgemm_i8_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) {
   if (st != QGEMM_OK) return st;
   if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
   if (!bytes) return QGEMM_ERR_NULL;
-  *bytes = i8_ws(N, K, M, false).total;
+  I8Params p{};
+  i8_plan(M, N, K, M, 1, 0, &p);
+  if (p.units == 0) return QGEMM_ERR_SHAPE;
+  *bytes = i8_ws(p, M, K).total;
   return QGEMM_OK;
 }
 
@@ -1322,7 +1330,9 @@ int qgemm_i8_moe_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) 
   if (st != QGEMM_OK) return st;
   if (M < 1 || M > 0x7FFFFFFF) return QGEMM_ERR_SHAPE;
   if (!bytes) return QGEMM_ERR_NULL;
-  *bytes = i8_ws(N, K, M, true).total;
+  I8Params p{};
+  i8_plan(M, N, K, M, 1, 1, &p);  // (the same for any expert count and rows of an expert)
+  *bytes = i8_ws(p, M, K).total;
   return QGEMM_OK;
 }
 

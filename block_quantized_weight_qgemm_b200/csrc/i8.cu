@@ -65,6 +65,31 @@ __device__ __forceinline__ uint2 i8_codes8(const uint4& v, float up, float inv, 
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
+// What a row's largest |x| (bf16 bits) makes of it.
+struct I8Row {
+  float scale;         // as it leaves: NaN for a row that is not finite
+  float up;            // a row near the bottom of the range is lifted by this exact power of two, scale and
+  float s, half, inv;  // all, so that the reciprocal is finite and the residual normal
+  bool none;           // all codes 0
+  __device__ __forceinline__ explicit I8Row(uint32_t bits) {
+    const float amax = __uint_as_float(bits << 16);
+    none = bits >= 0x7F80u || bits == 0;
+    scale = bits < 0x7F80u ? __fmul_rn(amax, kI8Inv) : __int_as_float(0x7FC00000);
+    up = amax >= 0x1p-60f ? 1.f : 0x1p64f;
+    s = scale * up;
+    half = 0.5f * s;
+    inv = none ? 0.f : __frcp_rn(s);
+  }
+  __device__ __forceinline__ uint2 codes(const uint4& v) const {
+    if (none) return make_uint2(0u, 0u);
+    return up == 1.f ? i8_codes8<false>(v, up, inv, s, half) : i8_codes8<true>(v, up, inv, s, half);
+  }
+};
+__device__ __forceinline__ uint32_t i8_max16(uint32_t top, const uint4& a) {  // two maxima of 16 bits
+  top = __vmaxu2(top, __vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu));
+  return __vmaxu2(top, __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+}
+
 // Per row: the largest |x| as bf16 bits (which order like the magnitudes, infinities and NaN above
 // every finite value), the scale, the codes.  A row is one warp's (WARP: short rows, eight to a
 // block) or a block's, each thread with up to R words of eight elements in registers; what is left of a
@@ -86,20 +111,16 @@ __global__ void __launch_bounds__(WARP ? 256 : kI8QuantThreads) qgemm_i8_quant_k
   const int k0 = (WARP ? lane : (int)threadIdx.x) * 8, step = WARP ? 256 : (int)blockDim.x * 8;
   const uint16_t* xr = p.x + m * p.K;
   uint4 v[R];
-  uint32_t top = 0;  // two maxima of 16 bits
-  auto take = [&](const uint4& a) {
-    top = __vmaxu2(top, __vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu));
-    top = __vmaxu2(top, __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
-  };
+  uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     const int k = k0 + j * step;
     v[j] = k < p.K ? *reinterpret_cast<const uint4*>(xr + k) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
-  for (int j = 0; j < R; ++j) take(v[j]);
+  for (int j = 0; j < R; ++j) top = i8_max16(top, v[j]);
   if (!WARP)
-    for (int k = k0 + R * step; k < p.K; k += step) take(*reinterpret_cast<const uint4*>(xr + k));
+    for (int k = k0 + R * step; k < p.K; k += step) top = i8_max16(top, *reinterpret_cast<const uint4*>(xr + k));
   uint32_t bits = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
   if (!WARP) {
     __shared__ uint32_t red[kI8QuantThreads / 32];
@@ -107,32 +128,17 @@ __global__ void __launch_bounds__(WARP ? 256 : kI8QuantThreads) qgemm_i8_quant_k
     __syncthreads();
     bits = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? red[lane] : 0u);
   }
-  const bool finite = bits < 0x7F80u;
-  const float amax = __uint_as_float(bits << 16);
-  const float scale = finite ? __fmul_rn(amax, kI8Inv) : __int_as_float(0x7FC00000);
-  if (k0 == 0) p.scales[m] = scale;
+  const I8Row row(bits);
+  if (k0 == 0) p.scales[m] = row.scale;
   int8_t* cr = p.codes + m * p.K;
-  auto write = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int k = k0 + j * step;
-      if (k < p.K) *reinterpret_cast<uint2*>(cr + k) = f(v[j]);
-    }
-    if (!WARP)
-      for (int k = k0 + R * step; k < p.K; k += step)
-        *reinterpret_cast<uint2*>(cr + k) = f(*reinterpret_cast<const uint4*>(xr + k));
-  };
-  if (!finite || bits == 0) {
-    write([](const uint4&) { return make_uint2(0u, 0u); });
-  } else if (amax >= 0x1p-60f) {
-    const float half = 0.5f * scale, inv = __frcp_rn(scale);
-    write([=](const uint4& a) { return i8_codes8<false>(a, 1.f, inv, scale, half); });
-  } else {
-    // a row near the bottom of the range is lifted by an exact power of two, scale and all, so
-    // that the reciprocal is finite and the residual normal
-    const float up = 0x1p64f, s = scale * up, half = 0.5f * s, inv = __frcp_rn(s);
-    write([=](const uint4& a) { return i8_codes8<true>(a, up, inv, s, half); });
+  for (int j = 0; j < R; ++j) {
+    const int k = k0 + j * step;
+    if (k < p.K) *reinterpret_cast<uint2*>(cr + k) = row.codes(v[j]);
   }
+  if (!WARP)
+    for (int k = k0 + R * step; k < p.K; k += step)
+      *reinterpret_cast<uint2*>(cr + k) = row.codes(*reinterpret_cast<const uint4*>(xr + k));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -179,6 +185,9 @@ constexpr int kI8Threads = (kI8EpiWarp0 + kI8EpiWarps) * 32;
 constexpr int kI8Strip = 128;  // rows per epilogue warp: half of a unit's 256 at most
 constexpr int kI8MaxStages = 12;
 constexpr int kI8List = 128;  // units of a CTA found ahead (routed)
+constexpr int kI8FusedRegs = 8;              // words of a row per lane of the fused quantisation
+constexpr int kI8FusedK = kI8FusedRegs * 256;
+constexpr int kI8FusedRows = 2 * (kI8Threads / 32 - kI8XWarp);
 
 __device__ __forceinline__ void i8_mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -293,13 +302,14 @@ __device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pr
 template <int NMAT>
 struct I8Scales {
   float sw[NMAT], sx[kI8Strip / 32];
-  __device__ __forceinline__ void fetch(const I8Params& p, const I8Unit<NMAT>& U, int64_t n, int hw, int lane) {
+  __device__ __forceinline__ void fetch(const I8Params& p, const float* xscales, const I8Unit<NMAT>& U, int64_t n,
+                                        int hw, int lane) {
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) sw[m] = n < p.N ? __ldg(U.sc[m] + n) : 0.f;
 #pragma unroll
     for (int e = 0; e < kI8Strip / 32; ++e) {
       const int row = (2 * (2 * e + (lane >> 4)) + hw) * 16 + (lane & 15);
-      sx[e] = row < U.rows ? p.xscales[U.row0 + row] : 0.f;
+      sx[e] = row < U.rows ? xscales[U.row0 + row] : 0.f;
     }
   }
 };
@@ -407,14 +417,17 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap tm_x) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t sbase = smem_u32(smem);
+  // fused: the codes of x, [chunk][NB][128] in the 128-byte swizzle; then the ring of stages
+  uint8_t* ring = smem + p.x_bytes;
+  const uint32_t xbase = smem_u32(smem), sbase = smem_u32(ring);
   const int NST = p.stages;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + (size_t)NST * p.stage_bytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + (size_t)NST * p.stage_bytes);
   const uint32_t bar_full = smem_u32(bars);
   const uint32_t bar_empty = bar_full + 8 * kI8MaxStages;
   const uint32_t bar_acc = bar_empty + 8 * kI8MaxStages;  // [2] a unit's accumulators are complete
   const uint32_t bar_acc_free = bar_acc + 16;             // [2] the epilogue has read them
   const uint32_t bar_drain = bar_acc_free + 16;
+  const uint32_t bar_x = bar_drain + 8;                   // fused: the codes of x are written
   int* ctl = reinterpret_cast<int*>(bars + 2 * kI8MaxStages + 6);
   volatile int* abort_flag = ctl + 1;
   // routed: the CTA's first units, then [E] the units before each expert's
@@ -426,9 +439,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const int first = (int)blockIdx.x / p.cs, stride = (int)gridDim.x / p.cs;
 
   if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tm_x);
+    if (!p.fused) prefetch_tmap(&tm_x);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, 2);  // both producers
+      mbar_init(bar_full + 8 * s, p.fused ? 1 : 2);  // the producers
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -436,6 +449,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       mbar_init(bar_acc_free + 8 * i, kI8EpiWarps);
     }
     mbar_init(bar_drain, 1);
+    mbar_init(bar_x, kI8Threads / 32 - kI8XWarp);
     ctl[1] = 0;
     fence_mbar_init();
   }
@@ -504,7 +518,46 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   bool held = false;  // (epilogue, clusters) its accumulators are complete and not read out yet
   const int q = warp & 3, hw = (warp - kI8EpiWarp0) >> 2, ch = q * 32 + lane;
 
-  if (warp == 0 || warp == kI8XWarp) {
+  // ------------------------------------------------------------ fused: quantise x
+  // The producer and the issuer go ahead; the other nine warps take two rows each.  Row r's byte k of
+  // a chunk goes to group (k / 16) ^ (r & 7) of its 128 bytes.
+  float* sx_own = reinterpret_cast<float*>(list);  // (a plain call has no list)
+  if (p.fused && warp >= kI8XWarp) {
+    griddep_wait();
+    const int c0 = rank * p.chunks / p.cs, c1 = (rank + 1) * p.chunks / p.cs;  // chunks of this CTA's ranges
+    constexpr int kWarps = kI8FusedRows / 2;  // a warp takes two rows at once
+    uint4 v[2][kI8FusedRegs];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kI8FusedRegs; ++j) {
+        const int r = warp - kI8XWarp + i * kWarps, at = (j * 32 + lane) * 8;
+        v[i][j] = r < p.M && at < p.K ? *reinterpret_cast<const uint4*>(p.x + (size_t)r * p.K + at)
+                                      : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = warp - kI8XWarp + i * kWarps;
+      if (r >= p.M) break;
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < kI8FusedRegs; ++j) top = i8_max16(top, v[i][j]);
+      const I8Row row(__reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16)));
+      if (lane == 0) sx_own[r] = row.scale;
+#pragma unroll
+      for (int j = 0; j < kI8FusedRegs; ++j) {
+        const int at = (j * 32 + lane) * 8, c = at >> 7, g = (at & 127) >> 4;
+        if (at < p.K && c >= c0 && c < c1)
+          *reinterpret_cast<uint2*>(smem + (size_t)((c - c0) * p.NB + r) * 128 + ((g ^ (r & 7)) << 4) + (at & 8)) =
+              row.codes(v[i][j]);
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read the codes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_x);
+  }
+
+  if (warp == 0 || (warp == kI8XWarp && !p.fused)) {
     // ------------------------------------------------------------ producers: weights, rows of x
     if (lane == 0) {
       const bool x = warp == kI8XWarp;
@@ -563,6 +616,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       for (int u = first; u < units && ok; u += stride, ++i) {
         const I8Unit<NMAT> U = unit(i, u);
         const uint32_t idesc = i8_idesc(128, (U.rows + 15) & ~15);
+        if (p.fused && i == 0 && !mbar_wait_spin(bar_x, 0, false, abort_flag, p.dev_err, kErrTimeout)) {
+          ok = false;
+          break;
+        }
         const uint32_t d = tmem + (uint32_t)((i & 1) * set);
         if (i >= 2) {
           if (!mbar_wait_spin(bar_acc_free + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, false, abort_flag,
@@ -579,7 +636,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           }
           tc_fence_after();
           const uint32_t st = sbase + (uint32_t)(sp.slot * p.stage_bytes);
-          const uint64_t bd = smem_desc_sw128(st + NMAT * kWCodeBytes);
+          const uint64_t bd = smem_desc_sw128(p.fused ? xbase + (uint32_t)((c - U.c0) * p.NB * 128)
+                                                      : st + NMAT * kWCodeBytes);
 #pragma unroll
           for (int m = 0; m < NMAT; ++m) {
             const uint64_t ad = smem_desc_sw128(st + m * kWCodeBytes);
@@ -601,18 +659,20 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp >= kI8EpiWarp0) {
     // ------------------------------------------------------------ epilogue
     // Two warps per lane quarter take alternate 16-row blocks of a unit.  A unit's scales are
     // loaded while the unit before it is computed and read out.
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
+    // fused: they come from these warps (and from warp 2, which has none of its own work here)
+    if (p.fused && !__all_sync(0xffffffffu, mbar_wait(bar_x, 0, abort_flag, p.dev_err, kErrTimeout))) units = 0;
     I8Unit<NMAT> U;
     I8Scales<NMAT> sc;
     auto fetch = [&](int i, int u) {
       U = unit(i, u);
-      sc.fetch(p, U, (int64_t)U.t * kTileRows + ch, hw, lane);
+      sc.fetch(p, p.fused ? sx_own : p.xscales, U, (int64_t)U.t * kTileRows + ch, hw, lane);
     };
     if (first < units) fetch(0, first);
     int i = 0;
@@ -644,7 +704,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     if (held) i8_send<NMAT>(p, V, d, hw, ch, sbase, rank);
     cluster_sync_all();
     if (held)
-      i8_read_out<NMAT>(p, V, d, hw, (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, smem, rank);
+      i8_read_out<NMAT>(p, V, d, hw, (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, ring, rank);
   }
 
   // ------------------------------------------------------------ teardown
@@ -809,7 +869,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     I8Scales<1> sc;
     auto fetch = [&](int u) {
       U = i8_unit<1>(p, nullptr, u);
-      sc.fetch(p, U, (int64_t)U.t * 2 * kTileRows + ch, hw, lane);
+      sc.fetch(p, p.xscales, U, (int64_t)U.t * 2 * kTileRows + ch, hw, lane);
     };
     if (pid < p.units) fetch(pid);
     int i = 0;
@@ -980,15 +1040,21 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
     }
   }
   p->w_again = p->b_tiles > 1;
-  p->stage_bytes = nmat * kWCodeBytes + (p->NB + p->box - 1) / p->box * p->box * 128;
+  // Small plain calls quantise x in the product's own kernel, each CTA for itself: one launch in place of two,
+  // and no workspace.  As long as a warp has one row, or two short ones: 512 x 1024 takes 6.1 us where two
+  // kernels take 7.1 (1 row) and 7.3 where they take 6.9 (16 rows, but 8.4 against 13 us of host time);
+  // 16 rows of 2048 take 9.3 against 8.0, so they keep two kernels.
+  const int64_t x_bytes = (p->chunks + p->cs - 1) / p->cs * (int64_t)p->NB * 128;
+  const bool few = rows <= kI8FusedRows / 2 || (rows <= kI8FusedRows && K <= kI8FusedK / 2);
+  p->fused = !routed && p->S == 1 && K <= kI8FusedK && few;
+  p->x_bytes = p->fused ? (int)x_bytes : 0;
+  p->stage_bytes = nmat * kWCodeBytes + (p->fused ? 0 : (p->NB + p->box - 1) / p->box * p->box * 128);
   int cols = 32;
   while (cols < 2 * nmat * p->NB) cols <<= 1;
   p->tmem_cols = cols;
 }
 
-size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M) {
-  I8Params p{};
-  i8_plan(M, N, K, M, 1, 0, &p);
+size_t i8_partial_bytes(const I8Params& p) {
   return (size_t)(p.units - p.full) * (size_t)p.NB * (p.pair ? 2 : 1) * kTileRows * 4;
 }
 
@@ -1026,7 +1092,8 @@ static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, 
   const cudaError_t e = raise_smem((const void*)qgemm_i8_kernel<NMAT>, set_mask, dev);
   if (e != cudaSuccess) return e;
   const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 +
-                      (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : 0);
+                      (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : p.fused ? kI8FusedRows * 4 : 0) +
+                      (size_t)p.x_bytes;
   // (a ring of half the shared memory, which lets the next product's CTAs in beside these, measured 3 to
   // 15 % slower: with memory busy, a chunk takes microseconds to arrive)
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);

@@ -34,13 +34,16 @@ struct I8Params {
   int units, full;  // plain: units; the first `full` take all of K, those after write partials
   int S;            // K ranges of a split tile
   int cs;           // CTAs of a cluster that share a unit's K (then one unit per cluster)
+  int fused;        // x is quantised in the product's kernel, from x
+  int x_bytes;      // shared memory of its codes
+  const uint16_t* x;  // bf16 [M][K] (fused)
   int stages, stage_bytes, tmem_cols;
   int w_again;      // a weight tile is read by more than one unit
   int* ws;          // partials [units - full][NB][channels of a tile]
 };
 
 void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p);
-size_t i8_partial_bytes(int64_t N, int64_t K, int64_t M);
+size_t i8_partial_bytes(const I8Params& p);
 cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorMap& map_w, cudaStream_t stream);
 
 }  // namespace qg

@@ -621,10 +621,12 @@ def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=
     assert x.dtype == torch.bfloat16 and K == w.K
     y = _routed_out(y, M, w.N, y_dtype, x)
     if workspace is None:
-        workspace = _scratch(i8_workspace_size(w.N, K, M), x, stream)
-    guard, st = _at(stream, x, w.codes, w.scales, y, workspace)
+        nbytes = i8_workspace_size(w.N, K, M)
+        workspace = _scratch(nbytes, x, stream) if nbytes else None
+    guard, st = _at(stream, x, w.codes, w.scales, y, x if workspace is None else workspace)
     _call("qgemm_i8_run", guard, x.data_ptr(), M, K, w.codes.data_ptr(), w.scales.data_ptr(), w.N, y.data_ptr(),
-          _row_dtype(y), workspace.data_ptr(), _nbytes(workspace), st)
+          _row_dtype(y), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else _nbytes(workspace), st)
     return y
 
 

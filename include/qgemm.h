@@ -385,7 +385,8 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
  * float [N].  qgemm_i8_pack quantises fp32 W the same way per channel; qgemm_i8_repack_rowmajor
  * brings int8 codes [N][code_pitch] of a checkpoint into the layout (its scales are used as
  * they are).  qgemm_i8_quant_x is the row quantisation alone: codes int8 [M][K], scales [M].
- * Workspaces hold the codes and scales of x and, where K is split, int32 partials.  Scales need 4-byte alignment, all else 16.
+ * Workspaces hold the codes and scales of x and, where K is split, int32 partials; a small call
+ * needs none (its size is 0 and workspace may be NULL).  Scales need 4-byte alignment, all else 16.
  * Errors as for qgemm_run.
  */
 int qgemm_i8_packed_size(int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes);

@@ -71,8 +71,8 @@ REFUSED = [
     (_run, dict(K=131088), SHAPE), (_run, dict(K=24), K_BLOCK), (_run, dict(ydt=2), FORMAT),
     (_run, dict(x=None), NULL), (_run, dict(c=None), NULL), (_run, dict(s=None), NULL),
     (_run, dict(y=None), NULL), (_run, dict(x=8), ALIGN), (_run, dict(c=8), ALIGN),
-    (_run, dict(y=8), ALIGN), (_run, dict(s=18), ALIGN), (_run, dict(ws=None), WORKSPACE),
-    (_run, dict(n=255), WORKSPACE), (_run, dict(ws=24), ALIGN),
+    (_run, dict(y=8), ALIGN), (_run, dict(s=18), ALIGN), (_run, dict(K=4096, ws=None), WORKSPACE),
+    (_run, dict(K=4096, n=255), WORKSPACE), (_run, dict(ws=24), ALIGN),
     (_moe, dict(M=0), SHAPE), (_moe, dict(E=0), SHAPE), (_moe, dict(E=4097), SHAPE), (_moe, dict(mr=0), SHAPE),
     (_moe, dict(K=131088), SHAPE), (_moe, dict(K=24), K_BLOCK), (_moe, dict(ydt=2), FORMAT),
     (_moe, dict(x=None), NULL), (_moe, dict(off=None), NULL), (_moe, dict(c=None), NULL),
@@ -101,6 +101,7 @@ def test_sizes(lib):
     at = [qgemm.i8_workspace_size(17408, 5120, M) for M in (1, 64, 65, 257, 8192)]
     assert at == sorted(at) and all(b >= M * 5124 for b, M in zip(at, (1, 64, 65, 257, 8192)))
     assert qgemm.i8_moe_workspace_size(512, 2048, 640) >= 640 * 2052
+    assert qgemm.i8_workspace_size(512, 1024, 16) == 0     # a small call's product quantises x itself
     assert lib.qgemm_i8_workspace_size(8, 64, 0, ctypes.byref(sz)) == SHAPE
     assert lib.qgemm_i8_moe_workspace_size(8, 64, 4, None) == NULL
     assert lib.qgemm_i8_quant_x(16, 4, 24, 16, 16, None) == K_BLOCK
