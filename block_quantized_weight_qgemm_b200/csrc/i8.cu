@@ -251,13 +251,13 @@ __device__ __forceinline__ int i8_expert_rows(const I8Params& p, int ex, int& lo
 
 // Unit u.  Routed: pre[e] is the number of units before expert e's.  Plain: the first `full` units
 // take all of K, the tiles after them are split in S ranges each.
-template <int NMAT>
+template <int NMAT, bool ROUTED>
 __device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pre, int u) {
   I8Unit<NMAT> U;
   U.c0 = 0;
   U.c1 = p.chunks;
   U.part = -1;
-  if (p.off) {
+  if constexpr (ROUTED) {
     int a = 0, b = p.E;  // the last e with pre[e] <= u
     while (b - a > 1) {
       const int m = (a + b) >> 1;
@@ -351,14 +351,14 @@ __device__ __forceinline__ void i8_send(const I8Params& p, const I8Unit<NMAT>& V
 
 // The read-out of one warp's part of a unit's accumulators (d: its lane quarter's first column).
 // ch: the lane's channel within the unit, of `width`; ring: where a cluster's other CTAs have sent their
-// sums for this rank's blocks (cs above 1).
-template <int NMAT>
+// sums for this rank's blocks (CL).
+template <int NMAT, bool CL, bool PARTS>
 __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT>& V, uint32_t d, int hw, int64_t n,
                                             int ch, int width, const float (&sw)[NMAT],
                                             const float (&sxl)[kI8Strip / 32], const uint8_t* ring, int rank) {
   const bool in = n < p.N;
   for (int cb = hw * 16; cb < V.rows; cb += 32) {
-    if (p.cs > 1 && (cb >> 4) % p.cs != rank) continue;
+    if (CL && (cb >> 4) % p.cs != rank) continue;
     __syncwarp();
     uint32_t v[NMAT][16];
 #pragma unroll
@@ -370,7 +370,7 @@ __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT
 #pragma unroll
     for (int r = 0; r < 16; ++r) sx[r] = __shfl_sync(0xffffffffu, sxb, ((b & 1) << 4) + r);
     tmem_ld_wait();
-    for (int o = 0; o < p.cs - 1; ++o)
+    for (int o = 0; CL && o < p.cs - 1; ++o)
 #pragma unroll
       for (int m = 0; m < NMAT; ++m) {
         const uint8_t* at = ring + i8_block_at<NMAT>(V.rows, p.cs, o, cb >> 4, m) + ch * 16;
@@ -399,7 +399,7 @@ __device__ __forceinline__ void i8_read_out(const I8Params& p, const I8Unit<NMAT
     if (NMAT == 2)
       store(reinterpret_cast<__nv_bfloat16*>(p.out) + at, p.N,
             [&](int r) { return __float2bfloat16_rn(silu_mul(y(0, r), y(NMAT - 1, r))); });
-    else if (V.part >= 0)
+    else if (PARTS && V.part >= 0)
       store(p.ws + ((size_t)V.part * p.NB + cb) * width + ch, width, [&](int r) { return (int)v[0][r]; });
     else if (p.out_bf16)
       store(reinterpret_cast<__nv_bfloat16*>(p.out) + at, p.N, [&](int r) { return __float2bfloat16_rn(y(0, r)); });
@@ -412,7 +412,11 @@ __device__ __forceinline__ void prefetch_l2(const void* a) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
 }
 
-template <int NMAT>
+// MODE and CL (clusters share units) are template parameters because the code that a launch does not run
+// costs it time all the same: with all of it in one kernel, 64 rows by 17408 x 5120 took 20.2 us for 18.7.
+enum I8Mode { kI8Plain, kI8Fused, kI8Routed };
+
+template <int NMAT, int MODE, bool CL>
 __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_constant__ I8Params p,
                                                                  const __grid_constant__ CUtensorMap tm_x) {
   extern __shared__ uint8_t smem_raw[];
@@ -435,13 +439,14 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   int* pre = reinterpret_cast<int*>(list + kI8List);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the CTA's (or its cluster's) place among the units
-  const int rank = p.cs > 1 ? (int)cluster_ctarank() : 0;
-  const int first = (int)blockIdx.x / p.cs, stride = (int)gridDim.x / p.cs;
+  const int rank = CL ? (int)cluster_ctarank() : 0;
+  const int first = CL ? (int)blockIdx.x / p.cs : (int)blockIdx.x;
+  const int stride = CL ? (int)gridDim.x / p.cs : (int)gridDim.x;
 
   if (warp == 0 && lane == 0) {
-    if (!p.fused) prefetch_tmap(&tm_x);
+    if (MODE != kI8Fused) prefetch_tmap(&tm_x);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar_full + 8 * s, p.fused ? 1 : 2);  // the producers
+      mbar_init(bar_full + 8 * s, MODE == kI8Fused ? 1 : 2);  // the producers
       mbar_init(bar_empty + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   }
   if (warp == 1) i8_tmem_alloc(smem_u32(ctl), (uint32_t)p.tmem_cols);
   int units = p.units;
-  if (p.off) {
+  if constexpr (MODE == kI8Routed) {
     // Units of each expert; one without rows, or whose table entries cannot be read, has none.
     // (The offsets and tables are complete: the quantisation kernel before this one let it launch
     // only after all earlier grids had ended.)
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     // every thread finds one unit of this CTA, so that the roles below read it in one step
     for (int i = threadIdx.x; i < kI8List; i += kI8Threads) {
       const int64_t u = (int64_t)first + (int64_t)i * stride;
-      if (u < units) list[i] = i8_unit<NMAT>(p, pre, (int)u);
+      if (u < units) list[i] = i8_unit<NMAT, true>(p, pre, (int)u);
     }
   }
   tc_fence_before();
@@ -506,8 +511,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
   const int set = NMAT * p.NB;  // columns of one accumulator set
   auto unit = [&](int i, int u) {
-    I8Unit<NMAT> U = p.off && i < kI8List ? list[i] : i8_unit<NMAT>(p, pre, u);
-    if (p.cs > 1) {
+    I8Unit<NMAT> U =
+        MODE == kI8Routed && i < kI8List ? list[i] : i8_unit<NMAT, MODE == kI8Routed>(p, pre, u);
+    if (CL) {
       U.c0 = (int)((int64_t)rank * p.chunks / p.cs);
       U.c1 = (int)((int64_t)(rank + 1) * p.chunks / p.cs);
     }
@@ -522,9 +528,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   // The producer and the issuer go ahead; the other nine warps take two rows each.  Row r's byte k of
   // a chunk goes to group (k / 16) ^ (r & 7) of its 128 bytes.
   float* sx_own = reinterpret_cast<float*>(list);  // (a plain call has no list)
-  if (p.fused && warp >= kI8XWarp) {
+  if (MODE == kI8Fused && warp >= kI8XWarp) {
     griddep_wait();
-    const int c0 = rank * p.chunks / p.cs, c1 = (rank + 1) * p.chunks / p.cs;  // chunks of this CTA's ranges
+    const int c0 = CL ? rank * p.chunks / p.cs : 0;  // chunks of this CTA's range
+    const int c1 = CL ? (rank + 1) * p.chunks / p.cs : p.chunks;
     constexpr int kWarps = kI8FusedRows / 2;  // a warp takes two rows at once
     uint4 v[2][kI8FusedRegs];
 #pragma unroll
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     if (lane == 0) mbar_arrive(bar_x);
   }
 
-  if (warp == 0 || (warp == kI8XWarp && !p.fused)) {
+  if (warp == 0 || (warp == kI8XWarp && MODE != kI8Fused)) {
     // ------------------------------------------------------------ producers: weights, rows of x
     if (lane == 0) {
       const bool x = warp == kI8XWarp;
@@ -616,7 +623,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       for (int u = first; u < units && ok; u += stride, ++i) {
         const I8Unit<NMAT> U = unit(i, u);
         const uint32_t idesc = i8_idesc(128, (U.rows + 15) & ~15);
-        if (p.fused && i == 0 && !mbar_wait_spin(bar_x, 0, false, abort_flag, p.dev_err, kErrTimeout)) {
+        if (MODE == kI8Fused && i == 0 && !mbar_wait_spin(bar_x, 0, false, abort_flag, p.dev_err, kErrTimeout)) {
           ok = false;
           break;
         }
@@ -636,7 +643,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           }
           tc_fence_after();
           const uint32_t st = sbase + (uint32_t)(sp.slot * p.stage_bytes);
-          const uint64_t bd = smem_desc_sw128(p.fused ? xbase + (uint32_t)((c - U.c0) * p.NB * 128)
+          const uint64_t bd = smem_desc_sw128(MODE == kI8Fused ? xbase + (uint32_t)((c - U.c0) * p.NB * 128)
                                                       : st + NMAT * kWCodeBytes);
 #pragma unroll
           for (int m = 0; m < NMAT; ++m) {
@@ -667,12 +674,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     griddep_wait();  // the scales of x come from the preceding grid
     griddep_launch_dependents();
     // fused: they come from these warps (and from warp 2, which has none of its own work here)
-    if (p.fused && !__all_sync(0xffffffffu, mbar_wait(bar_x, 0, abort_flag, p.dev_err, kErrTimeout))) units = 0;
+    if (MODE == kI8Fused &&
+        !__all_sync(0xffffffffu, mbar_wait(bar_x, 0, abort_flag, p.dev_err, kErrTimeout))) units = 0;
     I8Unit<NMAT> U;
     I8Scales<NMAT> sc;
     auto fetch = [&](int i, int u) {
       U = unit(i, u);
-      sc.fetch(p, p.fused ? sx_own : p.xscales, U, (int64_t)U.t * kTileRows + ch, hw, lane);
+      sc.fetch(p, MODE == kI8Fused ? sx_own : p.xscales, U, (int64_t)U.t * kTileRows + ch, hw, lane);
     };
     if (first < units) fetch(0, first);
     int i = 0;
@@ -684,12 +692,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (p.cs > 1) {
+      if (CL) {
         held = true;
         break;
       }
-      i8_read_out<NMAT>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw, (int64_t)V.t * kTileRows + ch, ch,
-                        kTileRows, vs.sw, vs.sx, nullptr, 0);
+      i8_read_out<NMAT, false, MODE == kI8Plain>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw,
+                                                 (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
@@ -697,14 +705,15 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   }
 
   // ------------------------------------------------------------ sum over the cluster
-  if (p.cs > 1) {
+  if (CL) {
     // every CTA has all its sums: the rings hold nothing any more
     cluster_sync_all();
     const uint32_t d = tmem + ((uint32_t)(q * 32) << 16);
     if (held) i8_send<NMAT>(p, V, d, hw, ch, sbase, rank);
     cluster_sync_all();
     if (held)
-      i8_read_out<NMAT>(p, V, d, hw, (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, ring, rank);
+      i8_read_out<NMAT, true, false>(p, V, d, hw, (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, ring,
+                                     rank);
   }
 
   // ------------------------------------------------------------ teardown
@@ -791,7 +800,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       if (x) griddep_wait();  // the codes of x come from the preceding grid
       for (int u = pid; u < p.units && ok; u += pairs) {
-        const I8Unit<1> U = i8_unit<1>(p, nullptr, u);
+        const I8Unit<1> U = i8_unit<1, false>(p, nullptr, u);
         const int64_t t = 2 * (int64_t)U.t + rank;
         const int half = ((U.rows + 31) & ~31) >> 1;  // rows of the MMA's N that each CTA holds
         for (int c = U.c0; c < U.c1; ++c) {
@@ -824,7 +833,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       int i = 0;
       for (int u = pid; u < p.units && ok; u += pairs, ++i) {
-        const I8Unit<1> U = i8_unit<1>(p, nullptr, u);
+        const I8Unit<1> U = i8_unit<1, false>(p, nullptr, u);
         const uint32_t idesc = i8_idesc(256, (U.rows + 31) & ~31);
         const uint32_t d = tmem + (uint32_t)((i & 1) * 256);
         if (i >= 2) {
@@ -868,7 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     I8Unit<1> U;
     I8Scales<1> sc;
     auto fetch = [&](int u) {
-      U = i8_unit<1>(p, nullptr, u);
+      U = i8_unit<1, false>(p, nullptr, u);
       sc.fetch(p, p.xscales, U, (int64_t)U.t * 2 * kTileRows + ch, hw, lane);
     };
     if (pid < p.units) fetch(pid);
@@ -881,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      i8_read_out<1>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
+      i8_read_out<1, false, true>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
                      2 * kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
@@ -1086,22 +1095,30 @@ static cudaError_t launch_gemm(void (*kern)(P...), size_t smem, int grid, int cl
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int NMAT>
-static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, cudaStream_t stream) {
+template <int NMAT, int MODE, bool CL>
+static cudaError_t launch_i8_kernel(I8Params& p, const CUtensorMap& map, int dev, cudaStream_t stream) {
   static std::atomic<uint64_t> set_mask{0};
-  const cudaError_t e = raise_smem((const void*)qgemm_i8_kernel<NMAT>, set_mask, dev);
+  const auto kern = qgemm_i8_kernel<NMAT, MODE, CL>;
+  const cudaError_t e = raise_smem((const void*)kern, set_mask, dev);
   if (e != cudaSuccess) return e;
-  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 +
-                      (p.off ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E : p.fused ? kI8FusedRows * 4 : 0) +
-                      (size_t)p.x_bytes;
+  const size_t own = MODE == kI8Routed  ? kI8List * sizeof(I8Unit<NMAT>) + 4 * (size_t)p.E
+                     : MODE == kI8Fused ? 4 * (size_t)kI8FusedRows + (size_t)p.x_bytes
+                                        : 0;
+  const size_t misc = 1024 + 8 * (2 * kI8MaxStages + 6) + 16 + own;
   // (a ring of half the shared memory, which lets the next product's CTAs in beside these, measured 3 to
   // 15 % slower: with memory busy, a chunk takes microseconds to arrive)
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
   // routed: an upper bound, the kernel counts the units that have rows
-  const int64_t most = p.off ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M) : p.units;
-  const int grid = p.cs > 1 ? (int)most * p.cs : (int)std::min<int64_t>(most, sm_count(dev));
-  return launch_gemm(qgemm_i8_kernel<NMAT>, misc + (size_t)p.stages * p.stage_bytes, grid, p.cs, stream, p, map);
+  const int64_t most = MODE == kI8Routed ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M) : p.units;
+  const int grid = CL ? (int)most * p.cs : (int)std::min<int64_t>(most, sm_count(dev));
+  return launch_gemm(kern, misc + (size_t)p.stages * p.stage_bytes, grid, p.cs, stream, p, map);
+}
+
+template <int NMAT, int MODE>
+static cudaError_t launch_i8_impl(I8Params& p, const CUtensorMap& map, int dev, cudaStream_t stream) {
+  return p.cs > 1 ? launch_i8_kernel<NMAT, MODE, true>(p, map, dev, stream)
+                  : launch_i8_kernel<NMAT, MODE, false>(p, map, dev, stream);
 }
 
 // p: planned (i8_plan), operands filled in; map_x: x's codes in boxes of 128 x p.box; map_w (pair):
@@ -1118,7 +1135,10 @@ cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorM
     const int grid = 2 * std::min(p.units, sm_count(dev) / 2);
     e = launch_gemm(qgemm_i8_pair_kernel, smem, grid, 1, stream, p, map_x, map_w);
   } else {
-    e = p.nmat == 2 ? launch_i8_impl<2>(p, map_x, dev, stream) : launch_i8_impl<1>(p, map_x, dev, stream);
+    e = p.nmat == 2 ? launch_i8_impl<2, kI8Routed>(p, map_x, dev, stream)
+        : p.off     ? launch_i8_impl<1, kI8Routed>(p, map_x, dev, stream)
+        : p.fused   ? launch_i8_impl<1, kI8Fused>(p, map_x, dev, stream)
+                    : launch_i8_impl<1, kI8Plain>(p, map_x, dev, stream);
   }
   if (e != cudaSuccess || p.S == 1) return e;
   return launch_dep(qgemm_i8_reduce_kernel,

@@ -112,8 +112,8 @@ def special_rows(K):
     return x.to(BF16)
 
 
-def test_special_rows():
-    K = 272
+@pytest.mark.parametrize("K", [272, 2080])  # quantised in the product's kernel, and in one of its own
+def test_special_rows(K):
     x = special_rows(K)
     codes, scales = qgemm.i8_quant_x(x.cuda())
     codes, scales = codes.cpu().double(), scales.cpu()
