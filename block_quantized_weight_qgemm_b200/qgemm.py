@@ -413,22 +413,10 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
 # ---- routed tokens: sorted by expert, and back --------------------------------------------
 #
 # These calls take a few microseconds on the device, so the marshalling is kept lean: integer
-# addresses, one pass of checks, sizes remembered per shape.
+# addresses, one pass of checks, sizes remembered per shape.  A call on another device than the
+# current one is made again with that device current (the library launches on the current device).
 
 _ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
-
-
-def _at(stream, *tensors):
-    """Checks that the tensors are contiguous on one CUDA device; returns (the device guard a call
-    needs, its stream handle).  The library launches on the current device."""
-    i = tensors[0].get_device()
-    for t in tensors:
-        if t.get_device() != i or not t.is_contiguous():
-            raise AssertionError("the tensors of a call are contiguous and on one device")
-    assert i >= 0, "the tensors of a call are on a CUDA device"
-    guard = None if i == _current_device() else torch.cuda.device(i)
-    return guard, _raw_stream(i) if stream is None else stream.cuda_stream
-
 
 # torch's own accessors behind torch.cuda.current_device() and current_stream(), without the stream
 # object (3 us); the device is initialised once a tensor lies on it
@@ -436,15 +424,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-def _call(name: str, guard, *args):
-    fn = getattr(_lib or lib(), name)
-    if guard is None:
-        status = fn(*args)
-    else:
-        with guard:
-            status = fn(*args)
-    if status != OK:
-        raise QgemmError(status, name)
+def _device(*tensors) -> int:
+    """The CUDA device of the tensors of a call, which all lie there and are contiguous."""
+    i = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != i or not t.is_contiguous():
+            raise AssertionError("the tensors of a call are contiguous and on one device")
+    assert i >= 0, "the tensors of a call are on a CUDA device"
+    return i
 
 
 def _row_dtype(t) -> int:
@@ -471,7 +458,6 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
     T, H = x.shape
     T2, k = experts.shape
-    dt = _row_dtype(x)
     assert T2 == T and experts.dtype == torch.int32
     if xs is None:
         xs = x.new_empty((T * k, H))
@@ -484,10 +470,14 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     if rows is None:
         rows = torch.empty_like(experts)
     else:
-        assert rows.dtype == torch.int32 and rows.shape == (T, k)
-    guard, st = _at(stream, x, experts, xs, offsets, rows)
-    _call("qgemm_moe_dispatch", guard, x.data_ptr(), dt, T, H, experts.data_ptr(), k, E, offsets.data_ptr(),
-          rows.data_ptr(), xs.data_ptr(), st)
+        assert rows.dtype == torch.int32 and rows.shape == experts.shape
+    i = _device(x, experts, xs, offsets, rows)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return moe_dispatch(x, experts, E, xs, offsets, rows, stream)
+    _check((_lib or lib()).qgemm_moe_dispatch(
+        x.data_ptr(), _row_dtype(x), T, H, experts.data_ptr(), k, E, offsets.data_ptr(), rows.data_ptr(),
+        xs.data_ptr(), _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_dispatch")
     return xs, offsets, rows
 
 
@@ -499,10 +489,10 @@ def _routed(a, rows):
     return T, k, H
 
 
-def _routed_out(out, T, H, dtype, like):
+def _out(out, M, N, dtype, like):
     if out is None:
-        return like.new_empty((T, H), dtype=dtype)
-    assert out.shape == (T, H)
+        return like.new_empty((M, N), dtype=dtype)
+    assert out.shape == (M, N)
     return out
 
 
@@ -510,10 +500,14 @@ def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | 
                       dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
     T, k, H = _routed(dxs, rows)
-    dx = _routed_out(dx, T, H, dx_dtype, dxs)
-    guard, st = _at(stream, dxs, rows, dx)
-    _call("qgemm_moe_dispatch_grad", guard, dxs.data_ptr(), _row_dtype(dxs), T, H, rows.data_ptr(), k,
-          dx.data_ptr(), _row_dtype(dx), st)
+    dx = _out(dx, T, H, dx_dtype, dxs)
+    i = _device(dxs, rows, dx)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return moe_dispatch_grad(dxs, rows, dx, stream=stream)
+    _check((_lib or lib()).qgemm_moe_dispatch_grad(
+        dxs.data_ptr(), _row_dtype(dxs), T, H, rows.data_ptr(), k, dx.data_ptr(), _row_dtype(dx),
+        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_dispatch_grad")
     return dx
 
 
@@ -521,11 +515,15 @@ def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
                 y: torch.Tensor | None = None, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_combine: y[t] = sum_j weights[t, j] * ys[rows[t, j]], weights fp32 [T, k]."""
     T, k, H = _routed(ys, rows)
-    assert weights.dtype == torch.float32 and weights.shape == (T, k)
-    y = _routed_out(y, T, H, y_dtype, ys)
-    guard, st = _at(stream, ys, rows, weights, y)
-    _call("qgemm_moe_combine", guard, ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(),
-          weights.data_ptr(), k, y.data_ptr(), _row_dtype(y), st)
+    assert weights.dtype == torch.float32 and weights.shape == rows.shape
+    y = _out(y, T, H, y_dtype, ys)
+    i = _device(ys, rows, weights, y)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return moe_combine(ys, rows, weights, y, stream=stream)
+    _check((_lib or lib()).qgemm_moe_combine(
+        ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k, y.data_ptr(), _row_dtype(y),
+        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_combine")
     return y
 
 
@@ -534,15 +532,23 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
     """qgemm_moe_combine_grad: the gradients (dys [T*k, H] in ys's type, dw fp32 [T, k]) of
     moe_combine, given dy [T, H]."""
     T, k, H = _routed(ys, rows)
-    assert weights.dtype == torch.float32 and weights.shape == (T, k) and dy.shape == (T, H)
-    dys = _routed_out(dys, T * k, H, ys.dtype, ys)
-    assert dys.dtype == ys.dtype
-    dw = _routed_out(dw, T, k, torch.float32, ys)
-    assert dw.dtype == torch.float32
-    guard, st = _at(stream, dy, ys, rows, weights, dys, dw)
-    _call("qgemm_moe_combine_grad", guard, dy.data_ptr(), _row_dtype(dy), ys.data_ptr(),
-          _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k, dys.data_ptr(),
-          dw.data_ptr(), st)
+    assert weights.dtype == torch.float32 and weights.shape == rows.shape and dy.shape == (T, H)
+    if dys is None:
+        dys = torch.empty_like(ys)
+    else:
+        assert dys.dtype == ys.dtype and dys.shape == ys.shape
+    if dw is None:
+        dw = torch.empty_like(weights)
+    else:
+        assert dw.dtype == torch.float32 and dw.shape == rows.shape
+    i = _device(dy, ys, rows, weights, dys, dw)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return moe_combine_grad(dy, ys, rows, weights, dys, dw, stream)
+    _check((_lib or lib()).qgemm_moe_combine_grad(
+        dy.data_ptr(), _row_dtype(dy), ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k,
+        dys.data_ptr(), dw.data_ptr(), _raw_stream(i) if stream is None else stream.cuda_stream),
+        "qgemm_moe_combine_grad")
     return dys, dw
 
 
@@ -575,8 +581,12 @@ def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weig
     assert W.dtype == torch.float32
     w = out or I8Weight(N, K, W.device)
     assert (w.N, w.K) == (N, K)
-    guard, st = _at(stream, W, w.codes, w.scales)
-    _call("qgemm_i8_pack", guard, W.data_ptr(), N, K, w.codes.data_ptr(), w.scales.data_ptr(), st)
+    i = _device(W, w.codes, w.scales)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_pack(W, w, stream)
+    _check(lib().qgemm_i8_pack(W.data_ptr(), N, K, w.codes.data_ptr(), w.scales.data_ptr(),
+                               _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_pack")
     return w
 
 
@@ -589,21 +599,38 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
     assert scales.dtype == torch.float32 and scales.shape == (N,)
     w = out or I8Weight(N, K, codes_rm.device)
     assert (w.N, w.K) == (N, K) and codes_rm.get_device() == scales.get_device()
+    i = _device(w.codes, scales)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_repack_rowmajor(codes_rm, scales, w, stream)
     w.scales = scales
-    guard, st = _at(stream, w.codes, scales)
-    _call("qgemm_i8_repack_rowmajor", guard, N, K, codes_rm.data_ptr(), codes_rm.stride(0) if N > 1 else K,
-          w.codes.data_ptr(), st)
+    _check(lib().qgemm_i8_repack_rowmajor(N, K, codes_rm.data_ptr(), codes_rm.stride(0) if N > 1 else K,
+                                          w.codes.data_ptr(),
+                                          _raw_stream(i) if stream is None else stream.cuda_stream),
+           "qgemm_i8_repack_rowmajor")
     return w
 
 
-def i8_quant_x(x: torch.Tensor, stream=None):
+def i8_quant_x(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+               stream=None):
     """qgemm_i8_quant_x: x bf16 [M, K] -> (codes int8 [M, K], scales fp32 [M])."""
     M, K = x.shape
     assert x.dtype == torch.bfloat16
-    codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    scales = torch.empty(M, dtype=torch.float32, device=x.device)
-    guard, st = _at(stream, x, codes, scales)
-    _call("qgemm_i8_quant_x", guard, x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), st)
+    if codes is None:
+        codes = x.new_empty((M, K), dtype=torch.int8)
+    else:
+        assert codes.dtype == torch.int8 and codes.shape == (M, K)
+    if scales is None:
+        scales = x.new_empty(M, dtype=torch.float32)
+    else:
+        assert scales.dtype == torch.float32 and scales.shape == (M,)
+    i = _device(x, codes, scales)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_quant_x(x, codes, scales, stream)
+    _check((_lib or lib()).qgemm_i8_quant_x(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(),
+                                            _raw_stream(i) if stream is None else stream.cuda_stream),
+           "qgemm_i8_quant_x")
     return codes, scales
 
 
@@ -618,15 +645,24 @@ def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=
            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """qgemm_i8_run: x bf16 [M, K], quantised per row on the fly -> y [M, N] (fp32 or bf16)."""
     M, K = x.shape
+    N, codes, scales = w.N, w.codes, w.scales
     assert x.dtype == torch.bfloat16 and K == w.K
-    y = _routed_out(y, M, w.N, y_dtype, x)
-    if workspace is None:
-        nbytes = i8_workspace_size(w.N, K, M)
-        workspace = _scratch(nbytes, x, stream) if nbytes else None
-    guard, st = _at(stream, x, w.codes, w.scales, y, x if workspace is None else workspace)
-    _call("qgemm_i8_run", guard, x.data_ptr(), M, K, w.codes.data_ptr(), w.scales.data_ptr(), w.N, y.data_ptr(),
-          _row_dtype(y), None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else _nbytes(workspace), st)
+    y = _out(y, M, N, y_dtype, x)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = workspace.data_ptr(), _nbytes(workspace)
+    else:
+        nbytes = i8_workspace_size(N, K, M)
+        if nbytes:
+            workspace = _scratch(nbytes, x, stream)
+            ws = workspace.data_ptr()
+    i = _device(x, codes, scales, y, x if workspace is None else workspace)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_run(x, w, y, workspace=workspace, stream=stream)
+    _check((_lib or lib()).qgemm_i8_run(
+        x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), N, y.data_ptr(), _row_dtype(y), ws, nbytes,
+        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_run")
     return y
 
 
@@ -650,38 +686,45 @@ def i8_moe_workspace_size(N: int, K: int, M: int) -> int:
     return b.value
 
 
-def _i8_moe(x, offsets, tab):
+def _i8_moe(x, offsets, tab, workspace, stream):
+    """(M, K, workspace) of a routed int8 call."""
     M, K = x.shape
     assert x.dtype == torch.bfloat16 and K == tab.K
     assert offsets.dtype == torch.int32 and offsets.numel() == tab.E + 1
-    return M, K
+    if workspace is None:
+        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x, stream)
+    return M, K, workspace
 
 
 def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_rows: int,
                y: torch.Tensor | None = None, y_dtype=torch.float32, workspace=None, stream=None):
     """qgemm_i8_moe_run: rows of x grouped by expert (int32 offsets[E+1] on the device)."""
-    M, K = _i8_moe(x, offsets, tab)
-    y = _routed_out(y, M, tab.N, y_dtype, x)
-    if workspace is None:
-        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x, stream)
-    guard, st = _at(stream, x, offsets, tab.codes, y, workspace)
-    _call("qgemm_i8_moe_run", guard, x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows,
-          tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N, y.data_ptr(), _row_dtype(y),
-          workspace.data_ptr(), _nbytes(workspace), st)
+    M, K, workspace = _i8_moe(x, offsets, tab, workspace, stream)
+    y = _out(y, M, tab.N, y_dtype, x)
+    i = _device(x, offsets, tab.codes, y, workspace)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_moe_run(x, offsets, tab, max_rows, y, workspace=workspace, stream=stream)
+    _check((_lib or lib()).qgemm_i8_moe_run(
+        x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows, tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N,
+        y.data_ptr(), _row_dtype(y), workspace.data_ptr(), _nbytes(workspace),
+        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_moe_run")
     return y
 
 
 def i8_moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: I8ExpertTable, up: I8ExpertTable,
                    max_rows: int, h: torch.Tensor | None = None, workspace=None, stream=None):
     """qgemm_i8_moe_gate_up: h = bf16(SiLU(g) * u) per routed row."""
-    M, K = _i8_moe(x, offsets, gate)
+    M, K, workspace = _i8_moe(x, offsets, gate, workspace, stream)
     assert (gate.N, gate.K, gate.E) == (up.N, up.K, up.E)
-    h = _routed_out(h, M, gate.N, torch.bfloat16, x)
+    h = _out(h, M, gate.N, torch.bfloat16, x)
     assert h.dtype == torch.bfloat16
-    if workspace is None:
-        workspace = _scratch(i8_moe_workspace_size(gate.N, K, M), x, stream)
-    guard, st = _at(stream, x, offsets, gate.codes, up.codes, h, workspace)
-    _call("qgemm_i8_moe_gate_up", guard, x.data_ptr(), M, K, gate.E, offsets.data_ptr(), max_rows,
-          gate.codes.data_ptr(), gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(),
-          gate.N, h.data_ptr(), workspace.data_ptr(), _nbytes(workspace), st)
+    i = _device(x, offsets, gate.codes, up.codes, h, workspace)
+    if i != _current_device():
+        with torch.cuda.device(i):
+            return i8_moe_gate_up(x, offsets, gate, up, max_rows, h, workspace, stream)
+    _check((_lib or lib()).qgemm_i8_moe_gate_up(
+        x.data_ptr(), M, K, gate.E, offsets.data_ptr(), max_rows, gate.codes.data_ptr(), gate.scales.data_ptr(),
+        up.codes.data_ptr(), up.scales.data_ptr(), gate.N, h.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_moe_gate_up")
     return h
