@@ -52,14 +52,17 @@
  *     the fixed scratch of qgemm_run_noalloc (see there).  Host state: each calling thread
  *     keeps its last few tile plans and encoded x tensor maps (TMA descriptors, keyed by
  *     the operand's address and geometry; they hold no device memory).
- *   - qgemm_run and qgemm_ffn_gate_up calls that may overlap on the device need their own
- *     workspaces; qgemm_run_noalloc calls share one scratch and must not overlap.
+ *   - qgemm_run, qgemm_ffn_gate_up and qgemm_i8_* calls that may overlap on the device need
+ *     their own workspaces; qgemm_run_noalloc calls share one scratch and must not overlap.
  *   - The GEMM kernels are programmatic dependents of the small x-preparation kernel
  *     launched just before them and start streaming weights before they wait for it.  x
  *     (and every buffer a call writes) is ordered after all earlier work on the stream; the
  *     packed weights are read assuming the kernel that wrote them has completed, which holds
  *     for every kernel that does not trigger its dependents' launch early (this library's
- *     packers, and any kernel launched without programmatic dependent launch).
+ *     packers, and any kernel launched without programmatic dependent launch).  The same holds
+ *     for the offsets and pointer tables of qgemm_moe_run and qgemm_moe_gate_up
+ *     (qgemm_moe_dispatch's kernels keep to it); the qgemm_i8_moe_* entry points read theirs
+ *     after all earlier work on the stream.
  */
 #ifndef QGEMM_H
 #define QGEMM_H
@@ -329,7 +332,8 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
 /*
  * Routed tokens: the rows the qgemm_moe_* entry points read, sorted by expert, and the way back
  * with the routing weights applied, each with its gradient (Strix Halo prefill journey, the
- * routed MoE around the expert kernels).  T tokens choose k experts each: slot (t, j), in the order
+ * routed ids and the weighted reduce around the expert kernels; the gradients have no passage).
+ * T tokens choose k experts each: slot (t, j), in the order
  * t k + j, belongs to expert experts_dev[t][j].  A slot whose expert lies outside [0, E) (-1 for
  * a padded token) belongs to none: it has no row and adds nothing.  A token may name an expert
  * more than once.  T k <= 2^31-1, 1 <= E <= QGEMM_MOE_MAX_EXPERTS, H >= 1 elements per row, of
@@ -373,7 +377,9 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
 
 /*
  * int8 weights with one fp32 scale per output channel, times bf16 rows quantised to int8 with one
- * scale per row on the fly (W8A8; the pages' W8A8 int8 MMA tiers):
+ * scale per row on the fly (W8A8).  The pages quantise activations to int8 for their DP4A verify
+ * tiers (Atlas issue, verify-tier section); the int8 weights per channel have no passage: they are
+ * what W8A8 checkpoints hold.
  *   sx[m] = fp32_RNE(max|x_m| * fp32_RNE(1/127)),  q[m][k] = RNE(x[m][k] / sx[m])  (ties to
  *           even, of the exact quotient); a zero row gets sx = 0 and q = 0; a row that holds an infinity or
  *           NaN gets sx = NaN and q = 0, so that its row of y is NaN and no other row is touched;
