@@ -525,3 +525,40 @@ def test_on_a_stream_of_its_own():
     torch.cuda.synchronize()
     for x, y in zip(xs, ys):
         check(y, *quantise(x), p, sw)
+
+
+def test_outputs_and_codes_past_two_to_the_31():
+    # y of 2.3e9 elements, and x of 2.3e9 codes
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for M, N, K in ((140000, 16400, 64), (140000, 130, 16400)):
+        assert M * max(N, K) > 2 ** 31
+        rm = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+        sw = torch.rand(N, device="cuda", generator=g) + 0.5
+        x = torch.randn(M, K, device="cuda", generator=g, dtype=BF16)
+        y = qgemm.i8_run(x, qgemm.i8_repack_rowmajor(rm, sw), y_dtype=BF16)
+        t = torch.cat([torch.arange(0, 9), torch.arange(M - 9, M), torch.arange(0, M, 9973)]).cuda()
+        check(y[t], *quantise(x[t].cpu()), rm.cpu().double(), sw.cpu())
+        off = torch.tensor([0, 70001, M], dtype=torch.int32, device="cuda")
+        tab = qgemm.I8ExpertTable([qgemm.i8_repack_rowmajor(rm, sw)] * 2)
+        assert torch.equal(qgemm.i8_moe_run(x, off, tab, M, y_dtype=BF16)[t], y[t])
+        del x, y
+
+
+def test_two_streams_at_once():
+    # products and sorts of two streams overlap on the device; each has its own buffers
+    w, p, sw = weight(640, 2048)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    xs = [inputs.activations(m, 2048, seed=m) for m in (7, 64, 700, 33, 300, 5)]
+    ids = torch.randint(0, 8, (3000, 4), dtype=torch.int32, generator=torch.Generator().manual_seed(1))
+    dev_x, dev_ids = [x.cuda() for x in xs], ids.cuda()
+    one = qgemm.moe_dispatch(torch.zeros(3000, 64, device="cuda"), dev_ids, 8)
+    torch.cuda.synchronize()
+    got = []
+    for r in range(6):
+        for i, x in enumerate(dev_x):
+            with torch.cuda.stream(streams[(i + r) % 2]):
+                got.append((i, qgemm.i8_run(x, w), qgemm.moe_dispatch(torch.zeros(3000, 64, device="cuda"), dev_ids, 8)))
+    torch.cuda.synchronize()
+    for i, y, (_, off, rows) in got:
+        check(y, *quantise(xs[i]), p, sw)
+        assert torch.equal(off, one[1]) and torch.equal(rows, one[2])

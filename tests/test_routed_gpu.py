@@ -247,3 +247,28 @@ def test_captured_replayed_and_on_another_stream():
         ref = x_h.double() * w_h.double().sum(1, keepdim=True)
         mag = x_h.double().abs() * w_h.double().abs().sum(1, keepdim=True)
         assert ((got[2].cpu().double() - ref).abs() <= (k + 1) * U * mag).all()
+
+
+def test_rows_past_two_to_the_31_elements():
+    # 1.2 million sorted rows of 2048: offsets that pass 32 bits, in elements and in bytes
+    T, k, H, E = 150000, 8, 2048, 16
+    assert T * k * H > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(0)
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=g, dtype=torch.int32)
+    x = torch.randn(T, H, device="cuda", generator=g).to(BF16)
+    xs, off, rows = qgemm.moe_dispatch(x, ids, E)
+    assert int(off[-1]) == T * k
+    t = torch.cat([torch.arange(0, 40), torch.arange(T - 40, T), torch.arange(0, T, 1499)]).cuda()
+    at = rows[t].long()
+    assert int(at.max()) * H > 2 ** 31
+    assert torch.equal(xs[at.reshape(-1)].view(-1, k, H), x[t][:, None, :].expand(-1, k, -1))
+    w = torch.rand(T, k, device="cuda", generator=g)
+    y = qgemm.moe_combine(xs, rows, w)[t].double()
+    ref = x[t].double() * w[t].double().sum(1, keepdim=True)
+    mag = x[t].double().abs() * w[t].double().sum(1, keepdim=True)
+    assert ((y - ref).abs() <= 2.0 ** -8 * ref.abs() + 1.01 * k * U * mag).all()
+    dys, dw = qgemm.moe_combine_grad(x, xs, rows, w)
+    want = x[t].double()[:, None, :] * w[t].double()[:, :, None]
+    assert ((dys[at.reshape(-1)].view(-1, k, H).double() - want).abs() <= (2.0 ** -8 + U) * (1 + U) * want.abs()).all()
+    sq = (x[t].double() ** 2).sum(1, keepdim=True)
+    assert ((dw[t].double() - sq).abs() <= H * U * sq).all()
