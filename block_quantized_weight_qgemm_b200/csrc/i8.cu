@@ -1027,8 +1027,10 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   p->chunks = (int)k_chunks(FMT_FP8, K);
   const int cap = nmat == 2 ? 128 : 256;
   p->NB = (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16);
-  // routed: small boxes, so that an expert's rows bring few of its neighbours' with them
-  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, 32) : p->NB;
+  // routed: boxes of half a tile at most, so that an expert's rows bring fewer of its neighbours' with them (8
+  // experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297, 260, 259 us -- a box
+  // has a cost of its own)
+  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, 128) : p->NB;
   p->b_tiles = (int)((rows + p->NB - 1) / p->NB);
   p->S = p->cs = 1;
   p->full = p->units = 0;
