@@ -267,10 +267,10 @@ __device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pr
     int lo;
     const int n = i8_expert_rows(p, a, lo);
     const int r = u - pre[a], bts = (n + p.NB - 1) / p.NB;
-    const int bt = r % bts;
+    const int bt = r % bts, nb = ((n + bts - 1) / bts + 15) & ~15;  // tiles of like size
     U.t = r / bts;
-    U.row0 = lo + bt * p.NB;
-    U.rows = min(p.NB, n - bt * p.NB);
+    U.row0 = lo + bt * nb;
+    U.rows = min(nb, n - bt * nb);
 #pragma unroll
     for (int m = 0; m < NMAT; ++m) {
       U.w[m] = p.codes_tab[m][a];
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------------------
-// Wide plain calls (more than 256 rows): the same roles on CTA pairs.  A tile is 256 channels (128 in
+// Wide plain calls (more than kI8PairRows rows): the same roles on CTA pairs.  A tile is 256 channels (128 in
 // each CTA's tensor memory) x 256 rows; each CTA loads its own 128 channels and half of the rows,
 // 32 KB per 128-K chunk where a lone CTA's 128 x 256 tile takes 48 KB for the same MMA time.  All
 // loads of a stage count on the even CTA's barrier (the tile-major codes by a tensor map too), so no
@@ -810,7 +810,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
             break;
           }
           const uint32_t st = sbase + (uint32_t)(sp.slot * kI8PairStage), fb = full0 + 8u * (uint32_t)sp.slot;
-          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * sp.slot, kI8PairStage);  // both halves
+          if (rank == 0)  // both halves
+            mbar_arrive_expect_tx(bar_full + 8 * sp.slot, x ? (uint32_t)p.box * 256u : 2u * kWCodeBytes);
           if (x)
             tma_load_2d_pair(st + kWCodeBytes, &tm_x, fb, c * 128, U.row0 + (int)rank * half, pol);
           else  // (a tile past the matrix reads zeros)
@@ -1016,17 +1017,23 @@ static int sm_count(int dev) {
 // Where all units fit on the device as clusters of several CTAs, a cluster splits each unit over K and sums
 // in distributed shared memory instead, without a second kernel, at the price of two cluster barriers.
 constexpr int kI8SplitChunks = 8, kI8ClusterChunks = 8;
+// Above this many rows the pairs' smaller loads per MMA win: 4096 x 4096 takes 17.2, 19.2 us (257, 384 rows)
+// by pairs, 14.5, 16.8 by lone CTAs; 17408 x 5120 37.5, 38.5 (450, 512) against 41.2, 45.4.
+constexpr int kI8PairRows = 384;
 // clusters of 0 .. 8 CTAs, one per SM, that a B200 holds at once (by its occupancy calculator)
 constexpr int kI8Clusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 
 // Tiling of a call: rows is M, or (E experts) the most rows an expert has.
 void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p) {
   const bool routed = E > 0;
-  p->pair = !routed && rows > 256;
+  p->pair = !routed && rows > kI8PairRows;
   p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
   p->chunks = (int)k_chunks(FMT_FP8, K);
   const int cap = nmat == 2 ? 128 : 256;
-  p->NB = (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16);
+  // tiles of like size: every unit of a round then takes as long (300 rows: two tiles of 160, not 256 and 44)
+  const int64_t b_tiles = (rows + cap - 1) / cap, step = p->pair ? 32 : 16;
+  p->NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16)
+                 : (int)((rows + b_tiles * step - 1) / (b_tiles * step) * step);
   // routed: boxes of half a tile at most, so that an expert's rows bring fewer of its neighbours' with them (8
   // experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297, 260, 259 us -- a box
   // has a cost of its own)

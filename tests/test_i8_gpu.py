@@ -170,7 +170,7 @@ def weight(N, K):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("N,K", [(1, 16), (64, 128), (129, 144), (300, 1040), (640, 2048), (128, 17408)])
-@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 100, 128, 129, 255, 256, 257, 300, 513])
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 100, 128, 129, 255, 256, 257, 300, 384, 385, 513])
 def test_run(M, N, K, dtype):
     w, p, sw = weight(N, K)
     x = inputs.activations(M, K, seed=M)
@@ -432,7 +432,8 @@ def test_k_split_over_clusters_and_not(M, N, K):
     check(y, q, sx, rm.cpu().double(), sw.cpu())
 
 
-@pytest.mark.parametrize("M,N,K", [(1000, 20000, 512), (257, 9600, 2048), (600, 1000, 8192), (64, 19000, 2048)])
+@pytest.mark.parametrize("M,N,K", [(1000, 20000, 512), (257, 9600, 2048), (450, 9600, 2048), (600, 1000, 8192),
+                                   (64, 19000, 2048)])
 def test_last_round_split_over_k(M, N, K):
     # full rounds of tiles, then a last round whose tiles are split over K and summed afterwards
     g = torch.Generator(device="cuda").manual_seed(N + M)
