@@ -234,6 +234,10 @@ __device__ __forceinline__ void i8_load_x(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
+// How a kernel finds its units: whole tiles, and tiles of a last round split over K; the same with x quantised
+// in the kernel; all tiles' chunks dealt out evenly, a run of them to each CTA; those of the experts.
+enum I8Mode { kI8Plain, kI8Fused, kI8Runs, kI8Routed };
+
 // One unit of work: rows row0 .. row0+rows-1 of x, a 128-channel tile (for a CTA pair: its two), chunks
 // c0 .. c1-1, and the buffers of each matrix.  part >= 0: the int32 partial it writes.
 template <int NMAT>
@@ -249,15 +253,22 @@ __device__ __forceinline__ int i8_expert_rows(const I8Params& p, int ex, int& lo
   return min(min(max(__ldg(p.off + ex + 1), lo), p.M) - lo, p.max_rows);
 }
 
+// First chunk (of all tiles' chunks in a row) of CTA i's run: at most 148 runs of 148 tiles of 1024 chunks, so
+// the product fits an int.
+__device__ __forceinline__ int i8_run_start(const I8Params& p, int i) {
+  return (int)((unsigned)(i * (p.tiles * p.b_tiles * p.chunks)) / (unsigned)p.runs);
+}
+
 // Unit u.  Routed: pre[e] is the number of units before expert e's.  Plain: the first `full` units
-// take all of K, the tiles after them are split in S ranges each.
-template <int NMAT, bool ROUTED>
+// take all of K, the tiles after them are split in S ranges each.  Runs: units i and runs + i are the parts of
+// CTA i's run in its first tile and in the next (a run is no longer than a tile).
+template <int NMAT, int MODE>
 __device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pre, int u) {
   I8Unit<NMAT> U;
   U.c0 = 0;
   U.c1 = p.chunks;
   U.part = -1;
-  if constexpr (ROUTED) {
+  if constexpr (MODE == kI8Routed) {
     int a = 0, b = p.E;  // the last e with pre[e] <= u
     while (b - a > 1) {
       const int m = (a + b) >> 1;
@@ -277,7 +288,15 @@ __device__ __forceinline__ I8Unit<NMAT> i8_unit(const I8Params& p, const int* pr
       U.sc[m] = p.scales_tab[m][a];
     }
   } else {
-    if (u >= p.full) {
+    if constexpr (MODE == kI8Runs) {
+      const int i = u < p.runs ? u : u - p.runs;
+      const int b0 = i8_run_start(p, i), b1 = i8_run_start(p, i + 1);
+      const int tile = b0 / p.chunks, at = tile * p.chunks;
+      U.part = 2 * i + (u < p.runs ? 0 : 1);
+      U.c0 = u < p.runs ? b0 - at : 0;
+      U.c1 = u < p.runs ? min(b1 - at, p.chunks) : b1 - at - p.chunks;
+      u = tile + (u < p.runs ? 0 : 1);
+    } else if (u >= p.full) {
       const int r = u - p.full, s = r % p.S;
       U.part = r;
       U.c0 = (int)((int64_t)s * p.chunks / p.S);
@@ -414,8 +433,6 @@ __device__ __forceinline__ void prefetch_l2(const void* a) {
 
 // MODE and CL (clusters share units) are template parameters because the code that a launch does not run
 // costs it time all the same: with all of it in one kernel, 64 rows by 17408 x 5120 took 20.2 us for 18.7.
-enum I8Mode { kI8Plain, kI8Fused, kI8Routed };
-
 template <int NMAT, int MODE, bool CL>
 __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_constant__ I8Params p,
                                                                  const __grid_constant__ CUtensorMap tm_x) {
@@ -460,6 +477,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   }
   if (warp == 1) i8_tmem_alloc(smem_u32(ctl), (uint32_t)p.tmem_cols);
   int units = p.units;
+  if constexpr (MODE == kI8Runs) {
+    // this CTA's run lies in one tile or two (or is empty: fewer chunks than CTAs)
+    const int b0 = i8_run_start(p, first), b1 = i8_run_start(p, first + 1);
+    units = b1 <= b0 ? 0 : (b1 - 1) / p.chunks > b0 / p.chunks ? 2 * p.runs : p.runs;
+  }
   if constexpr (MODE == kI8Routed) {
     // Units of each expert; one without rows, or whose table entries cannot be read, has none.
     // (The offsets and tables are complete: the quantisation kernel before this one let it launch
@@ -502,7 +524,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
     // every thread finds one unit of this CTA, so that the roles below read it in one step
     for (int i = threadIdx.x; i < kI8List; i += kI8Threads) {
       const int64_t u = (int64_t)first + (int64_t)i * stride;
-      if (u < units) list[i] = i8_unit<NMAT, true>(p, pre, (int)u);
+      if (u < units) list[i] = i8_unit<NMAT, MODE>(p, pre, (int)u);
     }
   }
   tc_fence_before();
@@ -512,7 +534,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   const int set = NMAT * p.NB;  // columns of one accumulator set
   auto unit = [&](int i, int u) {
     I8Unit<NMAT> U =
-        MODE == kI8Routed && i < kI8List ? list[i] : i8_unit<NMAT, MODE == kI8Routed>(p, pre, u);
+        MODE == kI8Routed && i < kI8List ? list[i] : i8_unit<NMAT, MODE>(p, pre, u);
     if (CL) {
       U.c0 = (int)((int64_t)rank * p.chunks / p.cs);
       U.c1 = (int)((int64_t)(rank + 1) * p.chunks / p.cs);
@@ -696,7 +718,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
         held = true;
         break;
       }
-      i8_read_out<NMAT, false, MODE == kI8Plain>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw,
+      i8_read_out<NMAT, false, MODE == kI8Plain || MODE == kI8Runs>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw,
                                                  (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
@@ -800,7 +822,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       if (x) griddep_wait();  // the codes of x come from the preceding grid
       for (int u = pid; u < p.units && ok; u += pairs) {
-        const I8Unit<1> U = i8_unit<1, false>(p, nullptr, u);
+        const I8Unit<1> U = i8_unit<1, kI8Plain>(p, nullptr, u);
         const int64_t t = 2 * (int64_t)U.t + rank;
         const int half = ((U.rows + 31) & ~31) >> 1;  // rows of the MMA's N that each CTA holds
         for (int c = U.c0; c < U.c1; ++c) {
@@ -834,7 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       bool ok = true;
       int i = 0;
       for (int u = pid; u < p.units && ok; u += pairs, ++i) {
-        const I8Unit<1> U = i8_unit<1, false>(p, nullptr, u);
+        const I8Unit<1> U = i8_unit<1, kI8Plain>(p, nullptr, u);
         const uint32_t idesc = i8_idesc(256, (U.rows + 31) & ~31);
         const uint32_t d = tmem + (uint32_t)((i & 1) * 256);
         if (i >= 2) {
@@ -878,7 +900,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     I8Unit<1> U;
     I8Scales<1> sc;
     auto fetch = [&](int u) {
-      U = i8_unit<1, false>(p, nullptr, u);
+      U = i8_unit<1, kI8Plain>(p, nullptr, u);
       sc.fetch(p, p.xscales, U, (int64_t)U.t * 2 * kTileRows + ch, hw, lane);
     };
     if (pid < p.units) fetch(pid);
@@ -921,16 +943,28 @@ __global__ void __launch_bounds__(256) qgemm_i8_reduce_kernel(const I8Params p) 
   griddep_wait();
   const int width = p.pair ? 2 * kTileRows : kTileRows;
   const int u = p.full + blockIdx.x;  // the tile
+  // its partials: S in a row, or (runs) one of each CTA whose run reaches into it
+  int first = blockIdx.x * p.S, count = p.S;
+  if (p.runs) {
+    const int a = u * p.chunks, b = a + p.chunks;
+    first = (int)((unsigned)(a * p.runs) / (unsigned)(p.tiles * p.b_tiles * p.chunks));
+    while (i8_run_start(p, first + 1) <= a) ++first;
+    for (count = 1; first + count < p.runs && i8_run_start(p, first + count) < b;) ++count;
+  }
   const int row0 = u % p.b_tiles * p.NB, rows = min(p.NB, p.M - row0);
   const int64_t n0 = (int64_t)(u / p.b_tiles) * width;
   const int quads = width / 4;  // threads along a row
   const int64_t n = n0 + threadIdx.x % quads * 4;
   for (int r = blockIdx.y * kI8ReduceRows + threadIdx.x / quads; r < min(rows, (int)(blockIdx.y + 1) * kI8ReduceRows);
        r += 256 / quads) {
-    const int* src = p.ws + (size_t)blockIdx.x * p.S * p.NB * width + (size_t)r * width + threadIdx.x % quads * 4;
+    const int* src = p.ws + (size_t)r * width + threadIdx.x % quads * 4;
     int4 a = make_int4(0, 0, 0, 0);
-    for (int s = 0; s < p.S; ++s) {
-      const int4 v = __ldcs(reinterpret_cast<const int4*>(src + (size_t)s * p.NB * width));
+    for (int s = 0; s < count; ++s) {
+      // a run that began in the tile before has this one as its second part
+      const int part = !p.runs ? first + s
+                               : 2 * (first + s) + (i8_run_start(p, first + s) < u * p.chunks ? 1 : 0);
+      if (p.runs && i8_run_start(p, first + s) == i8_run_start(p, first + s + 1)) continue;  // an empty run
+      const int4 v = __ldcs(reinterpret_cast<const int4*>(src + (size_t)part * p.NB * width));
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     }
     const int acc[4] = {a.x, a.y, a.z, a.w};
@@ -1057,6 +1091,23 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
       p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
     }
   }
+  // Tiles that fill neither the SMs nor clusters: all chunks dealt out evenly, where that saves more than the
+  // second part of a run, the reduction (6.5 us in all) and the partials' way through L2 (8 bytes per
+  // element at 3.5 TB/s) cost.  A chunk takes an SM 0.31 us to stream, or its bytes at 85 GB per ms where the
+  // rows of x make up the most of them.  10240 x 20480 with 1, 64, 256 rows: 52, 53, 69 us in whole tiles on 80
+  // SMs, 38, 46, 63 in runs on all; 12288 x 8192 stays with its 96 (23.4 against 23.0, 64 rows 24.3 against 28.9).
+  p->runs = 0;
+  if (!routed && !p->pair && all <= kI8SMs) {
+    const double us = std::max(0.31, (kWCodeBytes + p->NB * 128) / 85e3);
+    const int64_t now = p->cs > 1 ? (p->chunks + p->cs - 1) / p->cs + 3 : p->chunks;
+    const int64_t then = (all * p->chunks + kI8SMs - 1) / kI8SMs;
+    if ((now - then) * us > 6.5 + 2.0 * kI8SMs * p->NB * kTileRows * 8 / 3.5e6) {
+      p->runs = kI8SMs;
+      p->cs = 1;
+      p->full = 0;
+      p->units = 2 * kI8SMs;
+    }
+  }
   p->w_again = p->b_tiles > 1;
   // Small plain calls quantise x in the product's own kernel, each CTA for itself: one launch in place of two,
   // and no workspace.  As long as a warp has one row, or two short ones: 512 x 1024 takes 6.1 us where two
@@ -1064,7 +1115,7 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   // 16 rows of 2048 take 9.3 against 8.0, so they keep two kernels.
   const int64_t x_bytes = (p->chunks + p->cs - 1) / p->cs * (int64_t)p->NB * 128;
   const bool few = rows <= kI8FusedRows / 2 || (rows <= kI8FusedRows && K <= kI8FusedK / 2);
-  p->fused = !routed && p->S == 1 && K <= kI8FusedK && few;
+  p->fused = !routed && p->S == 1 && p->runs == 0 && K <= kI8FusedK && few;
   p->x_bytes = p->fused ? (int)x_bytes : 0;
   p->stage_bytes = nmat * kWCodeBytes + (p->fused ? 0 : (p->NB + p->box - 1) / p->box * p->box * 128);
   int cols = 32;
@@ -1119,8 +1170,12 @@ static cudaError_t launch_i8_kernel(I8Params& p, const CUtensorMap& map, int dev
   p.stages = (int)std::min<size_t>(kI8MaxStages, (kSmemLimit - 64 - misc) / (size_t)p.stage_bytes);
   if (p.stages < 2) return cudaErrorInvalidValue;
   // routed: an upper bound, the kernel counts the units that have rows
-  const int64_t most = MODE == kI8Routed ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M) : p.units;
-  const int grid = CL ? (int)most * p.cs : (int)std::min<int64_t>(most, sm_count(dev));
+  const int64_t most = MODE == kI8Routed ? (int64_t)p.tiles * p.b_tiles * std::min(p.E, p.M)
+                       : MODE == kI8Runs ? p.runs
+                                         : p.units;
+  const int grid = CL               ? (int)most * p.cs
+                   : MODE == kI8Runs ? p.runs
+                                     : (int)std::min<int64_t>(most, sm_count(dev));
   return launch_gemm(kern, misc + (size_t)p.stages * p.stage_bytes, grid, p.cs, stream, p, map);
 }
 
@@ -1147,11 +1202,13 @@ cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorM
     e = p.nmat == 2 ? launch_i8_impl<2, kI8Routed>(p, map_x, dev, stream)
         : p.off     ? launch_i8_impl<1, kI8Routed>(p, map_x, dev, stream)
         : p.fused   ? launch_i8_impl<1, kI8Fused>(p, map_x, dev, stream)
+        : p.runs    ? launch_i8_kernel<1, kI8Runs, false>(p, map_x, dev, stream)
                     : launch_i8_impl<1, kI8Plain>(p, map_x, dev, stream);
   }
-  if (e != cudaSuccess || p.S == 1) return e;
+  if (e != cudaSuccess || (p.S == 1 && !p.runs)) return e;
+  const int split = p.runs ? p.tiles * p.b_tiles : (p.units - p.full) / p.S;  // tiles with partials
   return launch_dep(qgemm_i8_reduce_kernel,
-                    dim3((unsigned)((p.units - p.full) / p.S), (unsigned)((p.NB + kI8ReduceRows - 1) / kI8ReduceRows)),
+                    dim3((unsigned)split, (unsigned)((p.NB + kI8ReduceRows - 1) / kI8ReduceRows)),
                     dim3(256), 0, stream, p);
 }
 

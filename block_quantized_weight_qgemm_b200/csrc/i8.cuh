@@ -33,6 +33,7 @@ struct I8Params {
   int b_tiles;      // row tiles of a plain call (routed: of an expert, at most)
   int units, full;  // plain: units; the first `full` take all of K, those after write partials
   int S;            // K ranges of a split tile
+  int runs;         // above 0: CTAs that all chunks are dealt out to (then units = 2 runs, each with a partial)
   int cs;           // CTAs of a cluster that share a unit's K (then one unit per cluster)
   int fused;        // x is quantised in the product's kernel, from x
   int x_bytes;      // shared memory of its codes

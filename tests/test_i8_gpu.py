@@ -420,7 +420,7 @@ def test_captured_gemm_shares_no_state_between_graphs():
 
 @pytest.mark.parametrize("M", [1, 16, 40, 129, 256])
 @pytest.mark.parametrize("N,K", [(100, 1280), (640, 1664), (1300, 2048), (2800, 1024), (5000, 1152), (5700, 1792),
-                                 (9400, 896), (9500, 1536)])
+                                 (9400, 896), (9500, 1536), (10000, 16400), (6500, 33000 // 16 * 16), (11000, 12288)])
 def test_k_split_over_clusters_and_not(M, N, K):
     # from 1 to 75 channel tiles: clusters of eight CTAs down to one share a tile's K, in uneven runs
     g = torch.Generator(device="cuda").manual_seed(N + M)
