@@ -20,7 +20,8 @@ namespace qg {
 
 // ---------------------------------------------------------------------------------------
 // Launch helper: every kernel here is a programmatic dependent of what precedes it.  Each waits
-// for that grid before it touches memory, and only then lets its own dependents launch.
+// for that grid before it touches memory (the gather after the sort reads x ahead: see there), and
+// only then, if at all, lets its own dependents launch.
 // ---------------------------------------------------------------------------------------
 template <typename... P, typename... A>
 static cudaError_t launch_dep(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
@@ -301,6 +302,8 @@ static RowShape row_shape(int64_t nvec) {
   return {bx, kRowThreads / bx};
 }
 
+// xs[row[s]] = x[t]: a row is read once and written k times.  Bound by HBM: 2048 tokens top-10 of 4 KB rows
+// (92 MB) in 14 us, the measured copy rate.
 template <typename V>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_gather_kernel(const V* __restrict__ x, int64_t T,
                                                                        int nvec, int k,
@@ -405,7 +408,8 @@ struct Vec<__nv_bfloat16, N> {
 };
 
 // y[t] = sum_j w[t][j] ys[row[t][j]], j ascending (w absent: 1); a row outside [0, S) is none.
-// The loads of B slots go together.
+// The loads of B slots go together.  Bound by HBM: 2048 tokens top-10 of 2048 bf16 in 16.5 us (85 % of the
+// measured copy rate), 16384 tokens top-8 of 4096 at it.
 template <typename TI, typename TO, int N, int B>
 __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI* __restrict__ ys, int64_t T,
                                                                         int H, int k, int64_t S,
@@ -448,7 +452,9 @@ __global__ void __launch_bounds__(kRowThreads) qgemm_moe_combine_kernel(const TI
 }
 
 // dys[row] = w dy and dw = <dy, ys[row]>: a warp per slot (the k warps of a token find its dy in L1).
-// A lane sums its elements in ascending order, the lanes are added in a fixed tree.
+// A lane sums its elements in ascending order, the lanes are added in a fixed tree.  Bound by HBM: 2048 tokens
+// top-10 of 2048 bf16 in 30 us (176 MB, 89 % of the measured copy rate); with a block per token and sums
+// over its warps it took 55.
 constexpr int kGradSteps = 2;  // steps of a row loaded together (34, 30, 34, 33 us with 1, 2, 4, 8: 2048 tokens, bf16)
 
 template <typename TD, typename TY, int N>
