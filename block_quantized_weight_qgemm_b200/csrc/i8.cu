@@ -178,6 +178,12 @@ __global__ void __launch_bounds__(256) qgemm_i8_pack_kernel(const float* __restr
 // per matrix) and warp 2 the rows of x (one or more boxes); apart, because the weights need not wait
 // for the quantisation kernel and fill the ring under it.  Warp 1 issues four M128 N(rows) K32 MMAs
 // per chunk and matrix, warps 3..10 read the accumulators out.
+//
+// Bound by the weights' stream up to about 100 rows: an SM takes 51 GB per ms through a ring of 200 KB, all of
+// them 7 TB/s.  17408 x 5120 (89 MB) takes 17.3 us with 1 row and 18.7 with 64, of which 12.6 are the stream
+// (its slope in K) and the rest the quantisation's and the launch's start and end; 512 routed experts of
+// 2 x 512 x 2048, 64 tokens top-10, run at the measured copy rate.  From there to 256 rows (25 us) by what
+// the SMs draw from L2, 11 to 13 TB/s: every tile reads all rows again.
 // ---------------------------------------------------------------------------------------
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8XWarp = 2, kI8EpiWarp0 = 3;
@@ -753,6 +759,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
 // 32 KB per 128-K chunk where a lone CTA's 128 x 256 tile takes 48 KB for the same MMA time.  All
 // loads of a stage count on the even CTA's barrier (the tile-major codes by a tensor map too), so no
 // thread stands between the copies and the MMAs.
+//
+// Bound by the tensor pipe and the power cap: 2048 rows by 17408 x 5120 take 120 us (3.0 POP/s) without the
+// quantisation, the pipe 85 % busy while the SMs are, at 1.64 GHz; run for seconds on end 150 us, where
+// cuBLAS takes 288 for the same product in bf16.
 // ---------------------------------------------------------------------------------------
 constexpr int kI8PairStage = 2 * kWCodeBytes;
 constexpr int kI8PairStages = 7;
@@ -1068,10 +1078,13 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   const int64_t b_tiles = (rows + cap - 1) / cap, step = p->pair ? 32 : 16;
   p->NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16)
                  : (int)((rows + b_tiles * step - 1) / (b_tiles * step) * step);
-  // routed: boxes of half a tile at most, so that an expert's rows bring fewer of its neighbours' with them (8
-  // experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297, 260, 259 us -- a box
-  // has a cost of its own)
-  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, 128) : p->NB;
+  // routed: boxes of about the mean expert's rows, so that its rows bring few of its neighbours' with them; but a
+  // box has a cost of its own.  8 experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297,
+  // 260, 259 us; 8 of 256 rows, 1024 x 1024: 12.5, 11.3, 10.9 (32, 64, 128); 512 of 40 rows, 2048 x 512: 116.8,
+  // 117.6, 123.5
+  const int64_t mean = routed ? M / E : 0;
+  const int box = mean >= 128 ? 128 : mean >= 64 ? 64 : 32;
+  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, box) : p->NB;
   p->b_tiles = (int)((rows + p->NB - 1) / p->NB);
   p->S = p->cs = 1;
   p->full = p->units = 0;
