@@ -1110,9 +1110,9 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x, int64_t M, int64_t K, const voi
 namespace {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool row_dtype(int d) { return d == QGEMM_Y_F32 || d == QGEMM_Y_BF16; }
-// T tokens of k slots, rows of H elements
+// T tokens of k slots, rows of H elements (at most 2^30: a thread's place in a row plus a grid's step stays an int)
 int check_routed(int64_t T, int k, int64_t H) {
-  if (T < 1 || k < 1 || H < 1 || H > 0x7FFFFFFF || T > 0x7FFFFFFF / k) return QGEMM_ERR_SHAPE;
+  if (T < 1 || k < 1 || H < 1 || H > (1 << 30) || T > 0x7FFFFFFF / k) return QGEMM_ERR_SHAPE;
   return QGEMM_OK;
 }
 }  // namespace

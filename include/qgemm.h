@@ -336,8 +336,8 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
  * T tokens choose k experts each: slot (t, j), in the order
  * t k + j, belongs to expert experts_dev[t][j].  A slot whose expert lies outside [0, E) (-1 for
  * a padded token) belongs to none: it has no row and adds nothing.  A token may name an expert
- * more than once.  T k <= 2^31-1, 1 <= E <= QGEMM_MOE_MAX_EXPERTS, H >= 1 elements per row, of
- * type QGEMM_Y_F32 or QGEMM_Y_BF16; int32 and weight arrays need 4-byte alignment, rows 16.
+ * more than once.  T k <= 2^31-1, 1 <= E <= QGEMM_MOE_MAX_EXPERTS, 1 <= H <= 2^30 elements per
+ * row, of type QGEMM_Y_F32 or QGEMM_Y_BF16; int32 and weight arrays need 4-byte alignment, rows 16.
  * Buffers written must not overlap buffers read.  Sums run in fp32 in a fixed order and round
  * once; equal inputs give equal bits.
  *

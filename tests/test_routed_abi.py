@@ -56,6 +56,8 @@ REFUSED = [
     (_dispatch, dict(off=18), ALIGN), (_dispatch, dict(rows=18), ALIGN),
     (_combine, dict(dt=2), FORMAT), (_combine, dict(ydt=-1), FORMAT), (_combine, dict(T=0), SHAPE),
     (_combine, dict(k=0), SHAPE), (_combine, dict(H=0), SHAPE), (_combine, dict(H=1 << 31), SHAPE),
+    (_dispatch, dict(H=(1 << 30) + 1), SHAPE), (_combine, dict(H=(1 << 30) + 1), SHAPE),
+    (_dgrad, dict(H=(1 << 31) - 1), SHAPE), (_cgrad, dict(H=(1 << 31) - 1), SHAPE),
     (_combine, dict(ys=None), NULL), (_combine, dict(rows=None), NULL), (_combine, dict(w=None), NULL),
     (_combine, dict(y=None), NULL), (_combine, dict(ys=8), ALIGN), (_combine, dict(y=8), ALIGN),
     (_combine, dict(rows=17), ALIGN), (_combine, dict(w=18), ALIGN),
