@@ -414,7 +414,8 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
 #
 # These calls take a few microseconds on the device, so the marshalling is kept lean: integer
 # addresses, one pass of checks, sizes remembered per shape.  A call on another device than the
-# current one is made again with that device current (the library launches on the current device).
+# current one is made again with that device current (the library launches on the current device), one
+# with a stream of its own with that stream current, so that what it allocates belongs to that stream.
 
 _ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
 
@@ -440,12 +441,16 @@ def _row_dtype(t) -> int:
     return d
 
 
-def _scratch(nbytes: int, like, stream):
-    """Device bytes for one call on `stream`, held until the call's work there is done."""
-    t = like.new_empty(max(nbytes, 16), dtype=torch.uint8)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _scratch(nbytes: int, like):
+    """Device bytes for one call."""
+    return like.new_empty(max(nbytes, 16), dtype=torch.uint8)
+
+
+def _on(stream, t, call, *args, **kwargs):
+    """`call` with `stream`, of t's device, as the current stream."""
+    assert stream.device == t.device, "the stream and the tensors of a call are on one device"
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
 
 
 def _nbytes(t) -> int:
@@ -456,6 +461,8 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
                  offsets: torch.Tensor | None = None, rows: torch.Tensor | None = None, stream=None):
     """qgemm_moe_dispatch: tokens x [T, H] (bf16 or fp32) and their experts int32 [T, k] (outside
     [0, E): none) -> (xs [T*k, H] sorted by expert, offsets int32 [E+1], rows int32 [T, k])."""
+    if stream is not None:
+        return _on(stream, x, moe_dispatch, x, experts, E, xs, offsets, rows)
     T, H = x.shape
     T2, k = experts.shape
     assert T2 == T and experts.dtype == torch.int32
@@ -474,10 +481,10 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     i = _device(x, experts, xs, offsets, rows)
     if i != _current_device():
         with torch.cuda.device(i):
-            return moe_dispatch(x, experts, E, xs, offsets, rows, stream)
+            return moe_dispatch(x, experts, E, xs, offsets, rows)
     _check((_lib or lib()).qgemm_moe_dispatch(
         x.data_ptr(), _row_dtype(x), T, H, experts.data_ptr(), k, E, offsets.data_ptr(), rows.data_ptr(),
-        xs.data_ptr(), _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_dispatch")
+        xs.data_ptr(), _raw_stream(i)), "qgemm_moe_dispatch")
     return xs, offsets, rows
 
 
@@ -499,31 +506,35 @@ def _out(out, M, N, dtype, like):
 def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | None = None,
                       dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
+    if stream is not None:
+        return _on(stream, dxs, moe_dispatch_grad, dxs, rows, dx, dx_dtype)
     T, k, H = _routed(dxs, rows)
     dx = _out(dx, T, H, dx_dtype, dxs)
     i = _device(dxs, rows, dx)
     if i != _current_device():
         with torch.cuda.device(i):
-            return moe_dispatch_grad(dxs, rows, dx, stream=stream)
+            return moe_dispatch_grad(dxs, rows, dx)
     _check((_lib or lib()).qgemm_moe_dispatch_grad(
         dxs.data_ptr(), _row_dtype(dxs), T, H, rows.data_ptr(), k, dx.data_ptr(), _row_dtype(dx),
-        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_dispatch_grad")
+        _raw_stream(i)), "qgemm_moe_dispatch_grad")
     return dx
 
 
 def moe_combine(ys: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor,
                 y: torch.Tensor | None = None, y_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """qgemm_moe_combine: y[t] = sum_j weights[t, j] * ys[rows[t, j]], weights fp32 [T, k]."""
+    if stream is not None:
+        return _on(stream, ys, moe_combine, ys, rows, weights, y, y_dtype)
     T, k, H = _routed(ys, rows)
     assert weights.dtype == torch.float32 and weights.shape == rows.shape
     y = _out(y, T, H, y_dtype, ys)
     i = _device(ys, rows, weights, y)
     if i != _current_device():
         with torch.cuda.device(i):
-            return moe_combine(ys, rows, weights, y, stream=stream)
+            return moe_combine(ys, rows, weights, y)
     _check((_lib or lib()).qgemm_moe_combine(
         ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k, y.data_ptr(), _row_dtype(y),
-        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_moe_combine")
+        _raw_stream(i)), "qgemm_moe_combine")
     return y
 
 
@@ -531,6 +542,8 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
                      dys: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
     """qgemm_moe_combine_grad: the gradients (dys [T*k, H] in ys's type, dw fp32 [T, k]) of
     moe_combine, given dy [T, H]."""
+    if stream is not None:
+        return _on(stream, dy, moe_combine_grad, dy, ys, rows, weights, dys, dw)
     T, k, H = _routed(ys, rows)
     assert weights.dtype == torch.float32 and weights.shape == rows.shape and dy.shape == (T, H)
     if dys is None:
@@ -544,10 +557,10 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, rows: torch.Tensor, wei
     i = _device(dy, ys, rows, weights, dys, dw)
     if i != _current_device():
         with torch.cuda.device(i):
-            return moe_combine_grad(dy, ys, rows, weights, dys, dw, stream)
+            return moe_combine_grad(dy, ys, rows, weights, dys, dw)
     _check((_lib or lib()).qgemm_moe_combine_grad(
         dy.data_ptr(), _row_dtype(dy), ys.data_ptr(), _row_dtype(ys), T, H, rows.data_ptr(), weights.data_ptr(), k,
-        dys.data_ptr(), dw.data_ptr(), _raw_stream(i) if stream is None else stream.cuda_stream),
+        dys.data_ptr(), dw.data_ptr(), _raw_stream(i)),
         "qgemm_moe_combine_grad")
     return dys, dw
 
@@ -577,6 +590,8 @@ class I8Weight:
 
 def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weight:
     """qgemm_i8_pack: W fp32 [N, K] on the device -> I8Weight."""
+    if stream is not None:
+        return _on(stream, W, i8_pack, W, out)
     N, K = W.shape
     assert W.dtype == torch.float32
     w = out or I8Weight(N, K, W.device)
@@ -584,9 +599,9 @@ def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weig
     i = _device(W, w.codes, w.scales)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_pack(W, w, stream)
+            return i8_pack(W, w)
     _check(lib().qgemm_i8_pack(W.data_ptr(), N, K, w.codes.data_ptr(), w.scales.data_ptr(),
-                               _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_pack")
+                               _raw_stream(i)), "qgemm_i8_pack")
     return w
 
 
@@ -594,6 +609,8 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
                        stream=None) -> I8Weight:
     """qgemm_i8_repack_rowmajor: a checkpoint's int8 codes [N, K] (rows may be strided) and fp32
     scales [N] -> I8Weight.  The scales are kept, not copied."""
+    if stream is not None:
+        return _on(stream, codes_rm, i8_repack_rowmajor, codes_rm, scales, out)
     N, K = codes_rm.shape
     assert codes_rm.dtype == torch.int8 and (codes_rm.stride(1) == 1 or K == 1)
     assert scales.dtype == torch.float32 and scales.shape == (N,)
@@ -602,11 +619,11 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
     i = _device(w.codes, scales)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_repack_rowmajor(codes_rm, scales, w, stream)
+            return i8_repack_rowmajor(codes_rm, scales, w)
     w.scales = scales
     _check(lib().qgemm_i8_repack_rowmajor(N, K, codes_rm.data_ptr(), codes_rm.stride(0) if N > 1 else K,
                                           w.codes.data_ptr(),
-                                          _raw_stream(i) if stream is None else stream.cuda_stream),
+                                          _raw_stream(i)),
            "qgemm_i8_repack_rowmajor")
     return w
 
@@ -614,6 +631,8 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
 def i8_quant_x(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
                stream=None):
     """qgemm_i8_quant_x: x bf16 [M, K] -> (codes int8 [M, K], scales fp32 [M])."""
+    if stream is not None:
+        return _on(stream, x, i8_quant_x, x, codes, scales)
     M, K = x.shape
     assert x.dtype == torch.bfloat16
     if codes is None:
@@ -627,9 +646,9 @@ def i8_quant_x(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch
     i = _device(x, codes, scales)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_quant_x(x, codes, scales, stream)
+            return i8_quant_x(x, codes, scales)
     _check((_lib or lib()).qgemm_i8_quant_x(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(),
-                                            _raw_stream(i) if stream is None else stream.cuda_stream),
+                                            _raw_stream(i)),
            "qgemm_i8_quant_x")
     return codes, scales
 
@@ -644,6 +663,8 @@ def i8_workspace_size(N: int, K: int, M: int) -> int:
 def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=torch.float32,
            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """qgemm_i8_run: x bf16 [M, K], quantised per row on the fly -> y [M, N] (fp32 or bf16)."""
+    if stream is not None:
+        return _on(stream, x, i8_run, x, w, y, y_dtype, workspace)
     M, K = x.shape
     N, codes, scales = w.N, w.codes, w.scales
     assert x.dtype == torch.bfloat16 and K == w.K
@@ -654,15 +675,15 @@ def i8_run(x: torch.Tensor, w: I8Weight, y: torch.Tensor | None = None, y_dtype=
     else:
         nbytes = i8_workspace_size(N, K, M)
         if nbytes:
-            workspace = _scratch(nbytes, x, stream)
+            workspace = _scratch(nbytes, x)
             ws = workspace.data_ptr()
     i = _device(x, codes, scales, y, x if workspace is None else workspace)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_run(x, w, y, workspace=workspace, stream=stream)
+            return i8_run(x, w, y, workspace=workspace)
     _check((_lib or lib()).qgemm_i8_run(
         x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), N, y.data_ptr(), _row_dtype(y), ws, nbytes,
-        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_run")
+        _raw_stream(i)), "qgemm_i8_run")
     return y
 
 
@@ -686,45 +707,49 @@ def i8_moe_workspace_size(N: int, K: int, M: int) -> int:
     return b.value
 
 
-def _i8_moe(x, offsets, tab, workspace, stream):
+def _i8_moe(x, offsets, tab, workspace):
     """(M, K, workspace) of a routed int8 call."""
     M, K = x.shape
     assert x.dtype == torch.bfloat16 and K == tab.K
     assert offsets.dtype == torch.int32 and offsets.numel() == tab.E + 1
     if workspace is None:
-        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x, stream)
+        workspace = _scratch(i8_moe_workspace_size(tab.N, K, M), x)
     return M, K, workspace
 
 
 def i8_moe_run(x: torch.Tensor, offsets: torch.Tensor, tab: I8ExpertTable, max_rows: int,
                y: torch.Tensor | None = None, y_dtype=torch.float32, workspace=None, stream=None):
     """qgemm_i8_moe_run: rows of x grouped by expert (int32 offsets[E+1] on the device)."""
-    M, K, workspace = _i8_moe(x, offsets, tab, workspace, stream)
+    if stream is not None:
+        return _on(stream, x, i8_moe_run, x, offsets, tab, max_rows, y, y_dtype, workspace)
+    M, K, workspace = _i8_moe(x, offsets, tab, workspace)
     y = _out(y, M, tab.N, y_dtype, x)
     i = _device(x, offsets, tab.codes, y, workspace)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_moe_run(x, offsets, tab, max_rows, y, workspace=workspace, stream=stream)
+            return i8_moe_run(x, offsets, tab, max_rows, y, workspace=workspace)
     _check((_lib or lib()).qgemm_i8_moe_run(
         x.data_ptr(), M, K, tab.E, offsets.data_ptr(), max_rows, tab.codes.data_ptr(), tab.scales.data_ptr(), tab.N,
         y.data_ptr(), _row_dtype(y), workspace.data_ptr(), _nbytes(workspace),
-        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_moe_run")
+        _raw_stream(i)), "qgemm_i8_moe_run")
     return y
 
 
 def i8_moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: I8ExpertTable, up: I8ExpertTable,
                    max_rows: int, h: torch.Tensor | None = None, workspace=None, stream=None):
     """qgemm_i8_moe_gate_up: h = bf16(SiLU(g) * u) per routed row."""
-    M, K, workspace = _i8_moe(x, offsets, gate, workspace, stream)
+    if stream is not None:
+        return _on(stream, x, i8_moe_gate_up, x, offsets, gate, up, max_rows, h, workspace)
+    M, K, workspace = _i8_moe(x, offsets, gate, workspace)
     assert (gate.N, gate.K, gate.E) == (up.N, up.K, up.E)
     h = _out(h, M, gate.N, torch.bfloat16, x)
     assert h.dtype == torch.bfloat16
     i = _device(x, offsets, gate.codes, up.codes, h, workspace)
     if i != _current_device():
         with torch.cuda.device(i):
-            return i8_moe_gate_up(x, offsets, gate, up, max_rows, h, workspace, stream)
+            return i8_moe_gate_up(x, offsets, gate, up, max_rows, h, workspace)
     _check((_lib or lib()).qgemm_i8_moe_gate_up(
         x.data_ptr(), M, K, gate.E, offsets.data_ptr(), max_rows, gate.codes.data_ptr(), gate.scales.data_ptr(),
         up.codes.data_ptr(), up.scales.data_ptr(), gate.N, h.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-        _raw_stream(i) if stream is None else stream.cuda_stream), "qgemm_i8_moe_gate_up")
+        _raw_stream(i)), "qgemm_i8_moe_gate_up")
     return h

@@ -563,3 +563,32 @@ def test_two_streams_at_once():
     for i, y, (_, off, rows) in got:
         check(y, *quantise(xs[i]), p, sw)
         assert torch.equal(off, one[1]) and torch.equal(rows, one[2])
+
+
+def test_a_call_on_another_stream_leaves_freed_blocks_alone():
+    # z is freed while a kernel of this stream is still to read it: its block is no scratch (nor output) for a
+    # call on another stream, which would write it at once
+    w, p, sw = weight(640, 2048)
+    x_h = inputs.activations(200, 2048, seed=3)
+    x = x_h.cuda()
+    side = torch.cuda.Stream()
+    nbytes = qgemm.i8_workspace_size(640, 2048, 200)
+    y_bytes = 200 * 640 * 4
+    torch.cuda.synchronize()
+    kept = []
+    for n in (nbytes, y_bytes):
+        kept.append(torch.empty(n, dtype=torch.uint8, device="cuda"))
+    torch.cuda.empty_cache()
+    zs = [torch.full((n,), 90 + i, dtype=torch.uint8, device="cuda") for i, n in enumerate((nbytes, y_bytes))]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # about 10 ms
+    for z, k in zip(zs, kept):
+        k.copy_(z)
+    del zs, z
+    y = qgemm.i8_run(x, w, stream=side)
+    torch.cuda.synchronize()
+    for i, k in enumerate(kept):
+        assert (k == 90 + i).all()
+    check(y, *quantise(x_h), p, sw)
+    with pytest.raises(AssertionError):
+        qgemm.i8_run(x_h, w, stream=side)
