@@ -1067,27 +1067,14 @@ constexpr int kI8PairRows = 384;
 // clusters of 0 .. 8 CTAs, one per SM, that a B200 holds at once (by its occupancy calculator)
 constexpr int kI8Clusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 
-// Tiling of a call: rows is M, or (E experts) the most rows an expert has.
-void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p) {
+// Tiles of NB rows: how many, and how K is shared.  Returns what `units` of them (expected of a routed call), that
+// run at once, take beyond a launch, in us.
+static double i8_tile(int64_t M, int64_t rows, int nmat, int E, int NB, int64_t units, I8Params* p) {
   const bool routed = E > 0;
-  p->pair = !routed && rows > kI8PairRows;
-  p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
-  p->chunks = (int)k_chunks(FMT_FP8, K);
-  const int cap = nmat == 2 ? 128 : 256;
-  // tiles of like size: every unit of a round then takes as long (300 rows: two tiles of 160, not 256 and 44)
-  const int64_t b_tiles = (rows + cap - 1) / cap, step = p->pair ? 32 : 16;
-  p->NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16)
-                 : (int)((rows + b_tiles * step - 1) / (b_tiles * step) * step);
-  // routed: boxes of about the mean expert's rows, so that its rows bring few of its neighbours' with them; but a
-  // box has a cost of its own.  8 experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297,
-  // 260, 259 us; 8 of 256 rows, 1024 x 1024: 12.5, 11.3, 10.9 (32, 64, 128); 512 of 40 rows, 2048 x 512: 116.8,
-  // 117.6, 123.5
-  const int64_t mean = routed ? M / E : 0;
-  const int box = mean >= 128 ? 128 : mean >= 64 ? 64 : 32;
-  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, box) : p->NB;
-  p->b_tiles = (int)((rows + p->NB - 1) / p->NB);
+  p->NB = NB;
+  p->b_tiles = (int)((rows + NB - 1) / NB);
   p->S = p->cs = 1;
-  p->full = p->units = 0;
+  p->full = p->units = p->runs = 0;
   const int64_t all = (int64_t)p->tiles * p->b_tiles;
   if (!p->pair) {
     const int64_t most = routed ? all * std::min<int64_t>(E, M) : all;
@@ -1104,23 +1091,72 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
       p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
     }
   }
+  // A chunk takes an SM 0.31 us to stream, or its bytes at 85 GB per ms where the rows of x make up the most of
+  // them (a pair's CTA: its bytes at 52).
+  const double us = p->pair ? (kWCodeBytes + NB * 64) / 52e3 : std::max(0.31 * nmat, (nmat * kWCodeBytes + NB * 128) / 85e3);
   // Tiles that fill neither the SMs nor clusters: all chunks dealt out evenly, where that saves more than the
   // second part of a run, the reduction (6.5 us in all) and the partials' way through L2 (8 bytes per
-  // element at 3.5 TB/s) cost.  A chunk takes an SM 0.31 us to stream, or its bytes at 85 GB per ms where the
-  // rows of x make up the most of them.  10240 x 20480 with 1, 64, 256 rows: 52, 53, 69 us in whole tiles on 80
+  // element at 3.5 TB/s) cost.  10240 x 20480 with 1, 64, 256 rows: 52, 53, 69 us in whole tiles on 80
   // SMs, 38, 46, 63 in runs on all; 12288 x 8192 stays with its 96 (23.4 against 23.0, 64 rows 24.3 against 28.9).
-  p->runs = 0;
   if (!routed && !p->pair && all <= kI8SMs) {
-    const double us = std::max(0.31, (kWCodeBytes + p->NB * 128) / 85e3);
     const int64_t now = p->cs > 1 ? (p->chunks + p->cs - 1) / p->cs + 3 : p->chunks;
     const int64_t then = (all * p->chunks + kI8SMs - 1) / kI8SMs;
-    if ((now - then) * us > 6.5 + 2.0 * kI8SMs * p->NB * kTileRows * 8 / 3.5e6) {
+    const double cost = 6.5 + 2.0 * kI8SMs * NB * kTileRows * 8 / 3.5e6;
+    if ((now - then) * us > cost) {
       p->runs = kI8SMs;
       p->cs = 1;
       p->full = 0;
       p->units = 2 * kI8SMs;
+      return then * us + cost;
     }
   }
+  const int share = p->cs * p->S;
+  double t = (p->chunks + share - 1) / share * us + (nmat == 2 ? 0.0175 : 0.006) * NB;
+  if (p->cs > 1) t += 2.85 + 0.016 * NB;
+  if (p->S > 1) t += 6.5 + (double)(p->units - p->full) * NB * kTileRows * (p->pair ? 16 : 8) / 3.5e6;
+  // beyond 64 SMs, the kernels before and after find fewer that are free: 2048 rows by 64 x 512 6.4 us in 32 pairs
+  // (tiles of 64 rows), 7.4 in 64 (32); 16 experts of 100 rows, 320 x 640 7.4 us on 96 SMs (64), 8.7 on 144 (48)
+  const int64_t sms = units * share * (p->pair ? 2 : 1);
+  return t + 0.014 * (double)std::max<int64_t>(0, sms - 64);
+}
+
+// Tiling of a call: rows is M, or (E experts) the most rows an expert has.
+void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p) {
+  const bool routed = E > 0;
+  p->pair = !routed && rows > kI8PairRows;
+  p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
+  p->chunks = (int)k_chunks(FMT_FP8, K);
+  const int cap = nmat == 2 ? 128 : 256;
+  // tiles of like size: every unit of a round then takes as long (300 rows: two tiles of 160, not 256 and 44)
+  const int64_t step = p->pair ? 32 : 16;
+  auto like = [&](int64_t b) { return (int)((rows + b * step - 1) / (b * step) * step); };
+  const int64_t b = (rows + cap - 1) / cap;
+  int NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16) : like(b);
+  // Tiles of fewer rows where that puts more SMs to work: as long as all units run at once, what counts is a
+  // unit's time (its bytes, its read-out).  256 rows by 512 x 1024: 8.7 us in tiles of 256, 6.5 of 32; 200 by
+  // 2048 x 2048 12.7 (208, clusters of 6) and 9.6 (64); 700 by 300 x 2960 21.0 (pairs of 256, K split) and 13.7
+  // (32); 8 experts of 256 rows, 1024 x 1024 11.1 (256) and 10.3 (144).  An expert is expected to have an
+  // eighth more rows than the mean.
+  const int64_t mean = routed ? M / E : 0;
+  const int64_t slots = p->pair ? kI8SMs / 2 : kI8SMs, experts = std::min<int64_t>(E, M);
+  auto count = [&](int nb) {
+    return p->tiles * (routed ? experts * ((mean + mean / 8 + nb - 1) / nb) : (rows + nb - 1) / nb);
+  };
+  double best = i8_tile(M, rows, nmat, E, NB, count(NB), p);
+  if (NB > 32 && count(NB) <= slots) {
+    for (int nb = like(b); nb >= 32 && count(nb) <= slots; nb = like((rows + nb - step - 1) / (nb - step))) {
+      const double t = i8_tile(M, rows, nmat, E, nb, count(nb), p);
+      if (t < best) best = t, NB = nb;
+      if (nb == 32) break;
+    }
+    i8_tile(M, rows, nmat, E, NB, count(NB), p);
+  }
+  // routed: boxes of about the mean expert's rows, so that its rows bring few of its neighbours' with them; but a
+  // box has a cost of its own.  8 experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297,
+  // 260, 259 us; 8 of 256 rows, 1024 x 1024: 12.5, 11.3, 10.9 (32, 64, 128); 512 of 40 rows, 2048 x 512: 116.8,
+  // 117.6, 123.5
+  const int box = mean >= 128 ? 128 : mean >= 64 ? 64 : 32;
+  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, box) : p->NB;
   p->w_again = p->b_tiles > 1;
   // Small plain calls quantise x in the product's own kernel, each CTA for itself: one launch in place of two,
   // and no workspace.  As long as a warp has one row, or two short ones: 512 x 1024 takes 6.1 us where two
