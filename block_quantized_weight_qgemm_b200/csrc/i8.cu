@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "common.cuh"
 #include "dequant.cuh"
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------------------
-// Wide plain calls (more than kI8PairRows rows): the same roles on CTA pairs.  A tile is 256 channels (128 in
+// Wide plain calls (more than kI8PairRows rows, see i8_plan): the same roles on CTA pairs.  A tile is 256 channels (128 in
 // each CTA's tensor memory) x 256 rows; each CTA loads its own 128 channels and half of the rows,
 // 32 KB per 128-K chunk where a lone CTA's 128 x 256 tile takes 48 KB for the same MMA time.  All
 // loads of a stage count on the even CTA's barrier (the tile-major codes by a tensor map too), so no
@@ -948,6 +949,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // Sum of the K ranges' partials of the split tiles (integers: any order gives the same bits),
 // scales, output.  One block per 8 rows of a split tile.
 constexpr int kI8ReduceRows = 8;
+constexpr int kI8ReduceLoads = 4;  // partials loaded together
 __global__ void __launch_bounds__(256) qgemm_i8_reduce_kernel(const I8Params p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -969,13 +971,18 @@ __global__ void __launch_bounds__(256) qgemm_i8_reduce_kernel(const I8Params p) 
        r += 256 / quads) {
     const int* src = p.ws + (size_t)r * width + threadIdx.x % quads * 4;
     int4 a = make_int4(0, 0, 0, 0);
-    for (int s = 0; s < count; ++s) {
-      // a run that began in the tile before has this one as its second part
-      const int part = !p.runs ? first + s
-                               : 2 * (first + s) + (i8_run_start(p, first + s) < u * p.chunks ? 1 : 0);
-      if (p.runs && i8_run_start(p, first + s) == i8_run_start(p, first + s + 1)) continue;  // an empty run
-      const int4 v = __ldcs(reinterpret_cast<const int4*>(src + (size_t)part * p.NB * width));
-      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    for (int s0 = 0; s0 < count; s0 += kI8ReduceLoads) {
+      int4 v[kI8ReduceLoads];
+#pragma unroll
+      for (int j = 0; j < kI8ReduceLoads; ++j) {
+        const int i = first + s0 + j;
+        // a run that began in the tile before has this one as its second part
+        const int part = !p.runs ? i : 2 * i + (i8_run_start(p, i) < u * p.chunks ? 1 : 0);
+        const bool none = s0 + j >= count || (p.runs && i8_run_start(p, i) == i8_run_start(p, i + 1));  // (an empty run)
+        v[j] = none ? make_int4(0, 0, 0, 0) : __ldcs(reinterpret_cast<const int4*>(src + (size_t)part * p.NB * width));
+      }
+#pragma unroll
+      for (int j = 0; j < kI8ReduceLoads; ++j) a.x += v[j].x, a.y += v[j].y, a.z += v[j].z, a.w += v[j].w;
     }
     const int acc[4] = {a.x, a.y, a.z, a.w};
     const float sx = p.xscales[row0 + r];
@@ -1076,6 +1083,9 @@ static double i8_tile(int64_t M, int64_t rows, int nmat, int E, int NB, int64_t 
   p->S = p->cs = 1;
   p->full = p->units = p->runs = 0;
   const int64_t all = (int64_t)p->tiles * p->b_tiles;
+  // A chunk takes an SM 0.31 us to stream, or its bytes at 85 GB per ms where the rows of x make up the most of
+  // them (a pair's CTA: at 76).
+  const double us = std::max(0.31 * nmat, p->pair ? (kWCodeBytes + NB * 64) / 76e3 : (nmat * kWCodeBytes + NB * 128) / 85e3);
   if (!p->pair) {
     const int64_t most = routed ? all * std::min<int64_t>(E, M) : all;
     for (int cs = 2; cs <= 8 && cs <= p->chunks; ++cs)
@@ -1084,16 +1094,16 @@ static double i8_tile(int64_t M, int64_t rows, int nmat, int E, int NB, int64_t 
   if (!routed) {
     const int64_t slots = p->pair ? kI8SMs / 2 : kI8SMs;
     const int64_t rest = all % slots;
-    const int64_t S = rest ? std::min<int64_t>(slots / rest, p->chunks) : 1;
+    // as many ranges as balance their own time and the partials' way through L2
+    const double way = rest * NB * kTileRows * (p->pair ? 16.0 : 8.0) / 3.5e6;
+    int64_t S = rest ? std::min<int64_t>({slots / rest, p->chunks, 1 + (int64_t)std::sqrt(p->chunks * us / way)}) : 1;
+    S = (p->chunks + (p->chunks + S - 1) / S - 1) / ((p->chunks + S - 1) / S);  // (no shorter ranges than needed)
     if (S > 1 && p->cs == 1 && p->chunks - (p->chunks + S - 1) / S > kI8SplitChunks) p->S = (int)S;
     if (all <= 0x3FFFFFFF) {
       p->full = (int)(p->S > 1 ? all - rest : all);
       p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
     }
   }
-  // A chunk takes an SM 0.31 us to stream, or its bytes at 85 GB per ms where the rows of x make up the most of
-  // them (a pair's CTA: its bytes at 52).
-  const double us = p->pair ? (kWCodeBytes + NB * 64) / 52e3 : std::max(0.31 * nmat, (nmat * kWCodeBytes + NB * 128) / 85e3);
   // Tiles that fill neither the SMs nor clusters: all chunks dealt out evenly, where that saves more than the
   // second part of a run, the reduction (6.5 us in all) and the partials' way through L2 (8 bytes per
   // element at 3.5 TB/s) cost.  10240 x 20480 with 1, 64, 256 rows: 52, 53, 69 us in whole tiles on 80
@@ -1123,33 +1133,47 @@ static double i8_tile(int64_t M, int64_t rows, int nmat, int E, int NB, int64_t 
 // Tiling of a call: rows is M, or (E experts) the most rows an expert has.
 void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p) {
   const bool routed = E > 0;
-  p->pair = !routed && rows > kI8PairRows;
-  p->tiles = (int)(p->pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
   p->chunks = (int)k_chunks(FMT_FP8, K);
   const int cap = nmat == 2 ? 128 : 256;
-  // tiles of like size: every unit of a round then takes as long (300 rows: two tiles of 160, not 256 and 44)
-  const int64_t step = p->pair ? 32 : 16;
-  auto like = [&](int64_t b) { return (int)((rows + b * step - 1) / (b * step) * step); };
-  const int64_t b = (rows + cap - 1) / cap;
-  int NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16) : like(b);
   // Tiles of fewer rows where that puts more SMs to work: as long as all units run at once, what counts is a
   // unit's time (its bytes, its read-out).  256 rows by 512 x 1024: 8.7 us in tiles of 256, 6.5 of 32; 200 by
   // 2048 x 2048 12.7 (208, clusters of 6) and 9.6 (64); 700 by 300 x 2960 21.0 (pairs of 256, K split) and 13.7
   // (32); 8 experts of 256 rows, 1024 x 1024 11.1 (256) and 10.3 (144).  An expert is expected to have an
   // eighth more rows than the mean.
-  const int64_t mean = routed ? M / E : 0;
-  const int64_t slots = p->pair ? kI8SMs / 2 : kI8SMs, experts = std::min<int64_t>(E, M);
-  auto count = [&](int nb) {
-    return p->tiles * (routed ? experts * ((mean + mean / 8 + nb - 1) / nb) : (rows + nb - 1) / nb);
-  };
-  double best = i8_tile(M, rows, nmat, E, NB, count(NB), p);
-  if (NB > 32 && count(NB) <= slots) {
-    for (int nb = like(b); nb >= 32 && count(nb) <= slots; nb = like((rows + nb - step - 1) / (nb - step))) {
+  const int64_t mean = routed ? M / E : 0;  // (at most: rows behind the last expert count)
+  const int64_t experts = std::min<int64_t>(E, M);
+  // (returns whether all units run at once)
+  auto tile = [&](bool pair) {
+    p->pair = pair;
+    p->tiles = (int)(pair ? (row_tiles(N) + 1) / 2 : row_tiles(N));
+    const int64_t slots = pair ? kI8SMs / 2 : kI8SMs;
+    // tiles of like size: every unit of a round then takes as long (300 rows: two tiles of 160, not 256 and 44)
+    const int64_t step = pair ? 32 : 16, b = (rows + cap - 1) / cap;
+    auto like = [&](int64_t b) { return (int)((rows + b * step - 1) / (b * step) * step); };
+    auto count = [&](int nb) {
+      return p->tiles * (routed ? experts * ((mean + mean / 8 + nb - 1) / nb) : (rows + nb - 1) / nb);
+    };
+    int NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16) : like(b);
+    double best = i8_tile(M, rows, nmat, E, NB, count(NB), p);
+    if (count(NB) > slots) return false;
+    for (int nb = like(b); !pair && NB > 32 && nb >= 32 && count(nb) <= slots;
+         nb = like((rows + nb - std::max(16, nb / 4) - 1) / (nb - std::max(16, nb / 4)))) {
       const double t = i8_tile(M, rows, nmat, E, nb, count(nb), p);
       if (t < best) best = t, NB = nb;
       if (nb == 32) break;
     }
     i8_tile(M, rows, nmat, E, NB, count(NB), p);
+    return true;
+  };
+  // Wide calls run on pairs, but where lone CTAs hold all tiles at once (700 by 300 x 2960 13.8 us on pairs, 11.3
+  // on lone CTAs; 2048 by 128 x 2048 12.6, 11.8; 700 by 6000 x 5120 23.5, 22.0; 1000 by 4700 x 5120, 76 tiles for
+  // 74 pairs, 43, 28.7); of tiles as large as theirs pairs still read less (500 by 9400 x 8192 32.6, 35.7).
+  const bool lone = tile(false);
+  if (!routed && rows > kI8PairRows) {
+    const bool large = p->NB > 192;
+    if (!lone || large) {
+      if (!tile(true) && lone) tile(false);
+    }
   }
   // routed: boxes of about the mean expert's rows, so that its rows bring few of its neighbours' with them; but a
   // box has a cost of its own.  8 experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297,
