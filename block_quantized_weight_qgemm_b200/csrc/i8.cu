@@ -1179,8 +1179,8 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   // box has a cost of its own.  8 experts of 1800 rows, 4096 x 5120 down: boxes of 32, 64, 128, 256 rows 391, 297,
   // 260, 259 us; 8 of 256 rows, 1024 x 1024: 12.5, 11.3, 10.9 (32, 64, 128); 512 of 40 rows, 2048 x 512: 116.8,
   // 117.6, 123.5
-  const int box = mean >= 128 ? 128 : mean >= 64 ? 64 : 32;
-  p->box = p->pair ? p->NB / 2 : routed ? std::min(p->NB, box) : p->NB;
+  const int most = mean >= 128 ? 128 : mean >= 64 ? 64 : 32, boxes = routed ? (p->NB + most - 1) / most : 1;
+  p->box = p->pair ? p->NB / 2 : (p->NB + boxes * 16 - 1) / (boxes * 16) * 16;
   p->w_again = p->b_tiles > 1;
   // Small plain calls quantise x in the product's own kernel, each CTA for itself: one launch in place of two,
   // and no workspace.  As long as a warp has one row, or two short ones: 512 x 1024 takes 6.1 us where two

@@ -592,3 +592,43 @@ def test_a_call_on_another_stream_leaves_freed_blocks_alone():
     check(y, *quantise(x_h), p, sw)
     with pytest.raises(AssertionError):
         qgemm.i8_run(x_h, w, stream=side)
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 100, 1040), (97, 513, 4096), (150, 64, 64), (200, 2048, 2048), (300, 1024, 5120),
+                                   (385, 129, 1040), (513, 640, 16400), (700, 300, 2960), (1000, 4700, 1040),
+                                   (1100, 4700, 1040), (2048, 64, 512), (2050, 130, 272), (4096, 1100, 528),
+                                   (450, 9600, 2064), (500, 9400, 1040), (1300, 5000, 1040)])
+def test_tiles_of_fewer_rows_and_wide_calls(M, N, K):
+    # few channels: tiles of 32 rows and more on many SMs, in clusters or not; wide calls on lone CTAs (up to 148
+    # tiles), on pairs, and on pairs with a last round of few tiles split over K
+    g = torch.Generator(device="cuda").manual_seed(N + M)
+    rm = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    sw = torch.rand(N, device="cuda", generator=g) + 0.5
+    x = inputs.activations(M, K, seed=M)
+    y = qgemm.i8_run(x.cuda(), qgemm.i8_repack_rowmajor(rm, sw))
+    q, sx = quantise(x)
+    check(y, q, sx, rm.cpu().double(), sw.cpu())
+
+
+@pytest.mark.parametrize("n,k", [(300, 272), (640, 1040)])
+@pytest.mark.parametrize("counts", [[70] * 7 + [0, 97], [256, 300, 211, 257], [20, 0, 45, 3, 17], [640, 12], [150] * 5,
+                                    [1, 500, 0, 0, 3, 2, 90]], ids=str)
+def test_moe_tiles_and_boxes(counts, n, k):
+    # experts of like and unlike size about the means at which tiles and boxes change
+    E, M = len(counts), sum(counts)
+    Ws = [[inputs.weights(n, k, seed=10 * e + j) for e in range(E)] for j in range(2)]
+    tabs = [qgemm.I8ExpertTable([qgemm.i8_pack(W.cuda()) for W in ws]) for ws in Ws]
+    refs = [[quantise(W) for W in ws] for ws in Ws]
+    x = inputs.activations(M, k, seed=M)
+    off = offsets_of(counts)
+    y = qgemm.i8_moe_run(x.cuda(), off, tabs[0], max(counts))
+    h = qgemm.i8_moe_gate_up(x.cuda(), off, *tabs, max(counts))
+    loose = qgemm.i8_moe_run(x.cuda(), off, tabs[0], M)  # an upper bound of the rows is enough
+    assert torch.equal(y, loose)
+    o = off.tolist()
+    for e in range(E):
+        a, b = o[e], o[e + 1]
+        if a < b:
+            q, sx = quantise(x[a:b])
+            check(y[a:b], q, sx, *refs[0][e])
+            h_check(h[a:b], *[(q @ p.t()) * s.double() * sx.double()[:, None] for p, s in (refs[0][e], refs[1][e])])
