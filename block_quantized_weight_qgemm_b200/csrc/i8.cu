@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(256) qgemm_i8_pack_kernel(const float* __restr
 // its weight scale stays in a register and a warp's stores are consecutive channels of one row.
 //
 // Persistent, one CTA per SM.  A unit is (expert, 128-channel tile, up to NB rows, K range); two
-// accumulator sets in tensor memory let the epilogue of a unit run under the MMAs of the next.
+// accumulator sets in tensor memory let the epilogue of a unit run under the MMAs of the next (one set
+// where i8_plan says so).
 // Warp 0 brings each 128-K chunk's weights into a ring of shared-memory stages (one 16 KB bulk copy
 // per matrix) and warp 2 the rows of x (one or more boxes); apart, because the weights need not wait
 // for the quantisation kernel and fill the ring under it.  Warp 1 issues four M128 N(rows) K32 MMAs
@@ -539,6 +540,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(ctl[0]);
   const int set = NMAT * p.NB;  // columns of one accumulator set
+  // use i of the accumulators: the set, and how often that has been used before
+  auto acc = [&](int i) { return NMAT == 2 && p.one_set ? 0 : i & 1; };
+  auto turn = [&](int i) { return NMAT == 2 && p.one_set ? i : i >> 1; };
   auto unit = [&](int i, int u) {
     I8Unit<NMAT> U =
         MODE == kI8Routed && i < kI8List ? list[i] : i8_unit<NMAT, MODE>(p, pre, u);
@@ -656,9 +660,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           ok = false;
           break;
         }
-        const uint32_t d = tmem + (uint32_t)((i & 1) * set);
-        if (i >= 2) {
-          if (!mbar_wait_spin(bar_acc_free + 8 * (i & 1), (uint32_t)((i >> 1) - 1) & 1u, false, abort_flag,
+        const uint32_t d = tmem + (uint32_t)(acc(i) * set);
+        if (turn(i) > 0) {
+          if (!mbar_wait_spin(bar_acc_free + 8 * acc(i), (uint32_t)(turn(i) - 1) & 1u, false, abort_flag,
                               p.dev_err, kErrTimeout)) {
             ok = false;
             break;
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
           sp.next(NST);
         }
         if (!ok) break;
-        i8_commit(bar_acc + 8 * (i & 1));
+        i8_commit(bar_acc + 8 * acc(i));
       }
       // every MMA has completed before the CTA may free its tensor memory
       i8_commit(bar_drain);
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       V = U;
       vs = sc;
       if (u + stride < units) fetch(i + 1, u + stride);
-      bool ok = mbar_wait(bar_acc + 8 * (i & 1), (uint32_t)(i >> 1) & 1u, abort_flag, p.dev_err, kErrTimeout);
+      bool ok = mbar_wait(bar_acc + 8 * acc(i), (uint32_t)turn(i) & 1u, abort_flag, p.dev_err, kErrTimeout);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -725,11 +729,11 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
         held = true;
         break;
       }
-      i8_read_out<NMAT, false, MODE == kI8Plain || MODE == kI8Runs>(p, V, tmem + lane_base + (uint32_t)((i & 1) * set), hw,
+      i8_read_out<NMAT, false, MODE == kI8Plain || MODE == kI8Runs>(p, V, tmem + lane_base + (uint32_t)(acc(i) * set), hw,
                                                  (int64_t)V.t * kTileRows + ch, ch, kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_acc_free + 8 * (i & 1));
+      if (lane == 0) mbar_arrive(bar_acc_free + 8 * acc(i));
     }
   }
 
@@ -1155,7 +1159,18 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
     };
     int NB = routed ? (int)std::min<int64_t>(cap, (rows + 15) / 16 * 16) : like(b);
     double best = i8_tile(M, rows, nmat, E, NB, count(NB), p);
-    if (count(NB) > slots) return false;
+    if (count(NB) > slots) {
+      // Two matrices: one set of accumulators in place of two holds tiles of up to 256 rows.  With nothing to
+      // overlap a read-out this costs more per round (64 experts of 128 rows, 1024 x 1024: 44.5 us in tiles of 128,
+      // 49.6 of 160), but pays where it makes one round of two (8 of 256 18.5 in tiles of 128, 15.9 of 144).
+      for (int nb = cap + 16; nmat == 2 && nb <= 256; nb += 16)
+        if (count(nb) <= slots) {
+          i8_tile(M, rows, nmat, E, nb, count(nb), p);
+          p->cs = 1;
+          return true;
+        }
+      return false;
+    }
     for (int nb = like(b); !pair && NB > 32 && nb >= 32 && count(nb) <= slots;
          nb = like((rows + nb - std::max(16, nb / 4) - 1) / (nb - std::max(16, nb / 4)))) {
       const double t = i8_tile(M, rows, nmat, E, nb, count(nb), p);
@@ -1192,7 +1207,8 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   p->x_bytes = p->fused ? (int)x_bytes : 0;
   p->stage_bytes = nmat * kWCodeBytes + (p->fused ? 0 : (p->NB + p->box - 1) / p->box * p->box * 128);
   int cols = 32;
-  while (cols < 2 * nmat * p->NB) cols <<= 1;
+  p->one_set = 2 * nmat * p->NB > 512;
+  while (cols < (p->one_set ? 1 : 2) * nmat * p->NB) cols <<= 1;
   p->tmem_cols = cols;
 }
 

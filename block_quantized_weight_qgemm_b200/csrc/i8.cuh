@@ -38,6 +38,7 @@ struct I8Params {
   int fused;        // x is quantised in the product's kernel, from x
   int x_bytes;      // shared memory of its codes
   const uint16_t* x;  // bf16 [M][K] (fused)
+  int one_set;      // one accumulator set instead of two (two matrices, tiles of more than 128 rows)
   int stages, stage_bytes, tmem_cols;
   int w_again;      // a weight tile is read by more than one unit
   int* ws;          // partials [units - full][NB][channels of a tile]

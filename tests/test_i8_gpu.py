@@ -632,3 +632,22 @@ def test_moe_tiles_and_boxes(counts, n, k):
             q, sx = quantise(x[a:b])
             check(y[a:b], q, sx, *refs[0][e])
             h_check(h[a:b], *[(q @ p.t()) * s.double() * sx.double()[:, None] for p, s in (refs[0][e], refs[1][e])])
+
+
+@pytest.mark.parametrize("counts,tiles", [([256, 230, 274, 264], 18), ([129] * 9, 16), ([140, 0, 131, 250, 100], 29),
+                                          ([129] * 8 + [700], 16)], ids=str)
+def test_gate_up_in_one_set_of_accumulators(counts, tiles):
+    # tiles of more than 128 rows, where experts and channels fill the SMs once; the expert of 700 rows makes more
+    E, M, n, k = len(counts), sum(counts), tiles * 128 - 5, 144
+    Ws = [[inputs.weights(n, k, seed=10 * e + j) for e in range(E)] for j in range(2)]
+    tabs = [qgemm.I8ExpertTable([qgemm.i8_pack(W.cuda()) for W in ws]) for ws in Ws]
+    refs = [[quantise(W) for W in ws] for ws in Ws]
+    x = inputs.activations(M, k, seed=M)
+    off = offsets_of(counts)
+    h = qgemm.i8_moe_gate_up(x.cuda(), off, *tabs, max(counts))
+    o = off.tolist()
+    for e in range(E):
+        if o[e] < o[e + 1]:
+            q, sx = quantise(x[o[e]:o[e + 1]])
+            h_check(h[o[e]:o[e + 1]],
+                    *[(q @ p.t()) * s.double() * sx.double()[:, None] for p, s in (refs[0][e], refs[1][e])])
