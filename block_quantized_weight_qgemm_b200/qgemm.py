@@ -453,6 +453,11 @@ def _on(stream, t, call, *args, **kwargs):
         return call(*args, **kwargs)
 
 
+def _new(M, N, dtype, like):
+    # (given its strides, torch makes a tensor in 1.5 us, without in 2.0 to 2.3)
+    return torch.empty_strided((M, N), (N, 1), dtype=dtype, device=like.device)
+
+
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
@@ -467,7 +472,7 @@ def moe_dispatch(x: torch.Tensor, experts: torch.Tensor, E: int, xs: torch.Tenso
     T2, k = experts.shape
     assert T2 == T and experts.dtype == torch.int32
     if xs is None:
-        xs = x.new_empty((T * k, H))
+        xs = _new(T * k, H, x.dtype, x)
     else:
         assert xs.dtype == x.dtype and xs.shape == (T * k, H)
     if offsets is None:
@@ -498,7 +503,7 @@ def _routed(a, rows):
 
 def _out(out, M, N, dtype, like):
     if out is None:
-        return like.new_empty((M, N), dtype=dtype)
+        return _new(M, N, dtype, like)
     assert out.shape == (M, N)
     return out
 
@@ -636,7 +641,7 @@ def i8_quant_x(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch
     M, K = x.shape
     assert x.dtype == torch.bfloat16
     if codes is None:
-        codes = x.new_empty((M, K), dtype=torch.int8)
+        codes = _new(M, K, torch.int8, x)
     else:
         assert codes.dtype == torch.int8 and codes.shape == (M, K)
     if scales is None:
