@@ -1072,7 +1072,7 @@ static int sm_count(int dev) {
 // Where all units fit on the device as clusters of several CTAs, a cluster splits each unit over K and sums
 // in distributed shared memory instead, without a second kernel, at the price of two cluster barriers.
 constexpr int kI8SplitChunks = 8, kI8ClusterChunks = 8;
-// Above this many rows the pairs' smaller loads per MMA win: 4096 x 4096 takes 17.2, 19.2 us (257, 384 rows)
+// Above this many rows the pairs' smaller loads per MMA win (but see i8_plan for calls of few tiles): 4096 x 4096 takes 17.2, 19.2 us (257, 384 rows)
 // by pairs, 14.5, 16.8 by lone CTAs; 17408 x 5120 37.5, 38.5 (450, 512) against 41.2, 45.4.
 constexpr int kI8PairRows = 384;
 // clusters of 0 .. 8 CTAs, one per SM, that a B200 holds at once (by its occupancy calculator)
