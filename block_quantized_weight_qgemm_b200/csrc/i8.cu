@@ -1075,8 +1075,10 @@ constexpr int kI8SplitChunks = 8, kI8ClusterChunks = 8;
 // Above this many rows the pairs' smaller loads per MMA win (but see i8_plan for calls of few tiles): 4096 x 4096 takes 17.2, 19.2 us (257, 384 rows)
 // by pairs, 14.5, 16.8 by lone CTAs; 17408 x 5120 37.5, 38.5 (450, 512) against 41.2, 45.4.
 constexpr int kI8PairRows = 384;
-// clusters of 0 .. 8 CTAs, one per SM, that a B200 holds at once (by its occupancy calculator)
-constexpr int kI8Clusters[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+// Clusters of 0 .. 8 CTAs, one per SM, that start together on a B200.  Its occupancy calculator says 45, 26 and 22 of
+// 3, 5 and 6, but the last ones of these wait for others to end: 64 rows, K = 8080, 14.9, 17.4, 18.6, 23.0 us with 42
+// to 45 clusters of 3 (46 of 2: 18.1); 251 rows 22.2, 24.0, 30.5 with 24 to 26 of 5, 18.6, 26.6 with 21, 22 of 6.
+constexpr int kI8Clusters[9] = {0, 148, 74, 42, 33, 24, 21, 15, 15};
 
 // Tiles of NB rows: how many, and how K is shared.  Returns what `units` of them (expected of a routed call), that
 // run at once, take beyond a launch, in us.
