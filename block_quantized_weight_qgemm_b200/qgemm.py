@@ -613,7 +613,8 @@ def i8_pack(W: torch.Tensor, out: I8Weight | None = None, stream=None) -> I8Weig
 def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weight | None = None,
                        stream=None) -> I8Weight:
     """qgemm_i8_repack_rowmajor: a checkpoint's int8 codes [N, K] (rows may be strided) and fp32
-    scales [N] -> I8Weight.  The scales are kept, not copied."""
+    scales [N] -> I8Weight.  Both are copied; with `out`, into its buffers, which tables and captured
+    graphs may hold the addresses of."""
     if stream is not None:
         return _on(stream, codes_rm, i8_repack_rowmajor, codes_rm, scales, out)
     N, K = codes_rm.shape
@@ -621,15 +622,16 @@ def i8_repack_rowmajor(codes_rm: torch.Tensor, scales: torch.Tensor, out: I8Weig
     assert scales.dtype == torch.float32 and scales.shape == (N,)
     w = out or I8Weight(N, K, codes_rm.device)
     assert (w.N, w.K) == (N, K) and codes_rm.get_device() == scales.get_device()
-    i = _device(w.codes, scales)
+    i = _device(w.codes, w.scales, scales)
     if i != _current_device():
         with torch.cuda.device(i):
             return i8_repack_rowmajor(codes_rm, scales, w)
-    w.scales = scales
     _check(lib().qgemm_i8_repack_rowmajor(N, K, codes_rm.data_ptr(), codes_rm.stride(0) if N > 1 else K,
                                           w.codes.data_ptr(),
                                           _raw_stream(i)),
            "qgemm_i8_repack_rowmajor")
+    with torch.inference_mode():  # (plain bytes, whatever mode or graph either tensor was made in)
+        w.scales.copy_(scales)
     return w
 
 
@@ -702,7 +704,8 @@ class I8ExpertTable:
         dev = experts[0].codes.device
         self.codes = torch.tensor([e.codes.data_ptr() for e in experts], dtype=torch.int64, device=dev)
         self.scales = torch.tensor([e.scales.data_ptr() for e in experts], dtype=torch.int64, device=dev)
-        self.experts = experts  # keeps the buffers alive
+        self.experts = experts
+        self.buffers = [(e.codes, e.scales) for e in experts]  # the addresses' tensors, kept alive
 
 
 @functools.lru_cache(maxsize=256)
