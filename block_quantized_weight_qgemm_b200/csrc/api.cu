@@ -1198,6 +1198,12 @@ I8Ws i8_ws(const I8Params& p, int64_t M, int64_t K) {
   w.total = w.partials + up(i8_partial_bytes(p));
   return w;
 }
+// What any plain call of at most M rows needs, p being the plan of M.  Partials come and go with the width (those of runs, of a last round
+// split over K), so their part is a bound: 128 channels x NB rows for each SM, two for each where runs are possible.
+size_t i8_ws_upto(const I8Params& p, int64_t M, int64_t N, int64_t K) {
+  if (p.fused) return 0;  // and so does every narrower call quantise x in the product's kernel
+  return i8_ws(p, M, K).partials + (i8_partial_bound(M, N, K) + 255) / 256 * 256;
+}
 // quantise x, then the GEMM that `p` describes (its x operand and tiling are filled in here)
 int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, void* workspace,
                 size_t workspace_bytes, void* stream) {
@@ -1305,7 +1311,7 @@ int qgemm_i8_workspace_size(int64_t N, int64_t K, int64_t M, size_t* bytes) {
   I8Params p{};
   i8_plan(M, N, K, M, 1, 0, &p);
   if (p.units == 0) return QGEMM_ERR_SHAPE;
-  *bytes = i8_ws(p, M, K).total;
+  *bytes = i8_ws_upto(p, M, N, K);
   return QGEMM_OK;
 }
 

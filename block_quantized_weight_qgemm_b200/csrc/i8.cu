@@ -1218,6 +1218,15 @@ size_t i8_partial_bytes(const I8Params& p) {
   return (size_t)(p.units - p.full) * (size_t)p.NB * (p.pair ? 2 : 1) * kTileRows * 4;
 }
 
+// Partials of at most M rows.  A split takes more than kI8SplitChunks chunks off a tile's time (runs, which cost 6.5 us,
+// more than 11), its units fit on the SMs at once, with 256 rows of 128 channels each or M in whole sixteens (a
+// pair's unit counts as two); runs have two for each SM, where the tiles are no more than the SMs.
+size_t i8_partial_bound(int64_t M, int64_t N, int64_t K) {
+  if (k_chunks(FMT_FP8, K) <= kI8SplitChunks + 1) return 0;
+  const size_t units = row_tiles(N) <= kI8SMs ? 2 * kI8SMs : kI8SMs;
+  return units * (size_t)std::min<int64_t>(256, (M + 15) / 16 * 16) * kTileRows * 4;
+}
+
 // Raises a kernel's dynamic shared-memory limit once per device (devices beyond 64: every time).
 static cudaError_t raise_smem(const void* kern, std::atomic<uint64_t>& set_mask, int dev) {
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;

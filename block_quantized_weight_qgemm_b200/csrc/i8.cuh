@@ -46,6 +46,7 @@ struct I8Params {
 
 void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8Params* p);
 size_t i8_partial_bytes(const I8Params& p);
+size_t i8_partial_bound(int64_t M, int64_t N, int64_t K);  // i8_partial_bytes of a plain call of at most M rows
 cudaError_t launch_i8_gemm(I8Params p, const CUtensorMap& map_x, const CUtensorMap& map_w, cudaStream_t stream);
 
 }  // namespace qg

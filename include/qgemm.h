@@ -392,7 +392,9 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
  * brings int8 codes [N][code_pitch] of a checkpoint into the layout (its scales are used as
  * they are).  qgemm_i8_quant_x is the row quantisation alone: codes int8 [M][K], scales [M].
  * Workspaces hold the codes and scales of x and, where K is split, int32 partials; a small call
- * needs none (its size is 0 and workspace may be NULL).  Scales need 4-byte alignment, all else 16.
+ * needs none (its size is 0 and workspace may be NULL).  qgemm_i8_workspace_size and
+ * qgemm_i8_moe_workspace_size give what any call of at most M rows needs, so one workspace of the
+ * widest call serves all.  Scales need 4-byte alignment, all else 16.
  * Errors as for qgemm_run.
  */
 int qgemm_i8_packed_size(int64_t N, int64_t K, size_t* code_bytes, size_t* scale_bytes);
