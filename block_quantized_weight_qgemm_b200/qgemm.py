@@ -420,9 +420,13 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
 _ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
 
 # torch's own accessors behind torch.cuda.current_device() and current_stream(), without the stream
-# object (3 us); the device is initialised once a tensor lies on it
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# object (3 us); the device is initialised once a tensor lies on it.  A torch without them (built for
+# the host alone) imports this module all the same, and has the public calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(i):
+        return torch.cuda.current_stream(i).cuda_stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device(*tensors) -> int:
