@@ -1145,8 +1145,10 @@ void i8_plan(int64_t M, int64_t N, int64_t K, int64_t rows, int nmat, int E, I8P
   // unit's time (its bytes, its read-out).  256 rows by 512 x 1024: 8.7 us in tiles of 256, 6.5 of 32; 200 by
   // 2048 x 2048 12.7 (208, clusters of 6) and 9.6 (64); 700 by 300 x 2960 21.0 (pairs of 256, K split) and 13.7
   // (32); 8 experts of 256 rows, 1024 x 1024 11.1 (256) and 10.3 (144).  An expert is expected to have an
-  // eighth more rows than the mean.
-  const int64_t mean = routed ? M / E : 0;  // (at most: rows behind the last expert count)
+  // eighth more rows than the mean (which counts rows behind the last expert too), and one at least where rows are
+  // fewer than experts: a mean of none took calls of hundreds of units for such as run at once (512 experts of
+  // 2 x 512 x 2048, 128 rows, max_rows 128: gate+up 48.8 us in tiles of 32, 44.6 of 128).
+  const int64_t mean = routed ? std::max<int64_t>(1, M / E) : 0;
   const int64_t experts = std::min<int64_t>(E, M);
   // (returns whether all units run at once)
   auto tile = [&](bool pair) {
