@@ -1210,8 +1210,9 @@ int i8_run_impl(const void* x, int64_t M, int64_t K, int64_t N, I8Params& p, voi
   const bool routed = p.off != nullptr;
   i8_plan(M, N, K, routed ? std::min<int64_t>(p.max_rows, M) : M, p.nmat, p.E, &p);
   // at most 2^30 units, and a row number plus a tile's rows stays an int
-  if (M > 0x7FFFFF00 || (routed ? (M / p.NB + std::min<int64_t>(p.E, M)) * p.tiles > 0x3FFFFFFF : p.units == 0))
+  if (M > 0x7FFFFF00 || (routed ? (M / p.NB + std::min<int64_t>(p.E, M)) * p.tiles > kI8MaxUnits : p.units == 0))
     return QGEMM_ERR_SHAPE;
+  p.falling = routed && (int64_t)p.E * p.b_tiles * p.tiles > kI8MaxUnits;
   const I8Ws w = i8_ws(p, M, K);
   if (w.total > 0 && (!workspace || workspace_bytes < w.total)) return QGEMM_ERR_WORKSPACE;
   if (workspace && !aligned16(workspace)) return QGEMM_ERR_ALIGN;

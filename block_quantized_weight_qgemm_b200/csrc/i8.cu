@@ -528,6 +528,23 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
       units += red[i];
     }
     for (int e = e0; e < e1; ++e) pre[e] += base;
+    // Falling offsets give rows to several experts: where that makes more units than there are clusters, which take one
+    // each, or (calls of hundreds of millions of rows) than an int counts, the call computes nothing.
+    bool many = CL && units > stride;
+    if (!CL && p.falling) {
+      int64_t all = 0;
+      for (int e = lane; e < p.E; e += 32) {
+        int lo;
+        all += (int64_t)((i8_expert_rows(p, e, lo) + p.NB - 1) / p.NB) * p.tiles;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      many = all > kI8MaxUnits;
+    }
+    if (many) {
+      if (threadIdx.x == 0) atomicExch(p.dev_err, kErrArg);
+      units = 0;
+    }
     __syncthreads();
     // every thread finds one unit of this CTA, so that the roles below read it in one step
     for (int i = threadIdx.x; i < kI8List; i += kI8Threads) {
@@ -1105,7 +1122,7 @@ static double i8_tile(int64_t M, int64_t rows, int nmat, int E, int NB, int64_t 
     int64_t S = rest ? std::min<int64_t>({slots / rest, p->chunks, 1 + (int64_t)std::sqrt(p->chunks * us / way)}) : 1;
     S = (p->chunks + (p->chunks + S - 1) / S - 1) / ((p->chunks + S - 1) / S);  // (no shorter ranges than needed)
     if (S > 1 && p->cs == 1 && p->chunks - (p->chunks + S - 1) / S > kI8SplitChunks) p->S = (int)S;
-    if (all <= 0x3FFFFFFF) {
+    if (all <= kI8MaxUnits) {
       p->full = (int)(p->S > 1 ? all - rest : all);
       p->units = (int)(p->S > 1 ? p->full + rest * p->S : all);
     }

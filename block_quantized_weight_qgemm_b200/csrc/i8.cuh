@@ -8,6 +8,7 @@ namespace qg {
 
 constexpr int kI8SMs = 148;  // of a B200, for the rules that weigh tilings
 constexpr int64_t kI8MaxK = 131072;  // |sum| <= K * 128 * 127 stays inside int32
+constexpr int kI8MaxUnits = 0x3FFFFFFF;  // of a call: a unit's number plus a grid's step stays an int
 
 struct I8Params {
   int M, N, K, chunks;
@@ -23,6 +24,7 @@ struct I8Params {
   // expert e, whose buffers come from the tables
   const int* off;
   int E, max_rows;
+  int falling;      // with offsets that fall, the experts' units could pass kI8MaxUnits
   const uint8_t* const* codes_tab[2];
   const float* const* scales_tab[2];
   // Tiling (i8_plan)

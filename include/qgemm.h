@@ -413,7 +413,9 @@ int qgemm_i8_run(const void* x_dev, int64_t M, int64_t K, const void* codes_dev,
  * The routed forms, with rows grouped by expert, pointer tables, max_rows and refusal of bad
  * table entries as for qgemm_moe_run and qgemm_moe_gate_up (the tables hold each expert's codes,
  * 16-byte aligned, and scales, 4-byte aligned; E <= QGEMM_MOE_MAX_EXPERTS).  Rows no expert
- * owns are left as they were.
+ * owns are left as they were.  Offsets that fall give rows to several experts: where those make
+ * more work than a launch counts, nothing is computed and the device status becomes
+ * QGEMM_ERR_DEVICE_ARG.
  *   qgemm_i8_moe_run:     y[m] = the product above with row m's expert.
  *   qgemm_i8_moe_gate_up: h[m] = bf16_RNE(SiLU(g) * u), g and u fp32 as y above.
  */
