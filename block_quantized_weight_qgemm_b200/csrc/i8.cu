@@ -20,7 +20,7 @@
 namespace qg {
 
 // ---------------------------------------------------------------------------------------
-// Activations: one CTA per row
+// Activations: a warp or a block per row
 // ---------------------------------------------------------------------------------------
 constexpr float kI8Inv = 1.f / 127.f;
 constexpr int kI8QuantThreads = 1024;  // at most
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) qgemm_i8_kernel(const __grid_co
 // thread stands between the copies and the MMAs.
 //
 // Bound by the tensor pipe and the power cap: 2048 rows by 17408 x 5120 take 120 us (3.0 POP/s) without the
-// quantisation, the pipe 85 % busy while the SMs are, at 1.64 GHz; run for seconds on end 150 us, where
+// quantisation, the pipe 79 % busy while the SMs are, at 1.63 GHz; run for seconds on end 150 us, where
 // cuBLAS takes 288 for the same product in bf16.
 // ---------------------------------------------------------------------------------------
 constexpr int kI8PairStage = 2 * kWCodeBytes;
@@ -945,8 +945,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      i8_read_out<1, false, true>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw, (int64_t)V.t * 2 * kTileRows + ch, ch,
-                     2 * kTileRows, vs.sw, vs.sx, nullptr, 0);
+      i8_read_out<1, false, true>(p, V, tmem + lane_base + (uint32_t)((i & 1) * 256), hw,
+                                  (int64_t)V.t * 2 * kTileRows + ch, ch, 2 * kTileRows, vs.sw, vs.sx, nullptr, 0);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -1070,7 +1070,6 @@ cudaError_t launch_i8_quant(const uint16_t* x, int64_t M, int64_t K, int8_t* cod
   return block(qgemm_i8_quant_kernel<4, false>, 4);
 }
 
-
 // SMs of device `dev`, read once per device (devices beyond 64 read it on every launch).
 static int sm_count(int dev) {
   static std::atomic<int> cached[64];
@@ -1089,8 +1088,8 @@ static int sm_count(int dev) {
 // Where all units fit on the device as clusters of several CTAs, a cluster splits each unit over K and sums
 // in distributed shared memory instead, without a second kernel, at the price of two cluster barriers.
 constexpr int kI8SplitChunks = 8, kI8ClusterChunks = 8;
-// Above this many rows the pairs' smaller loads per MMA win (but see i8_plan for calls of few tiles): 4096 x 4096 takes 17.2, 19.2 us (257, 384 rows)
-// by pairs, 14.5, 16.8 by lone CTAs; 17408 x 5120 37.5, 38.5 (450, 512) against 41.2, 45.4.
+// Above this many rows the pairs' smaller loads per MMA win (but see i8_plan for calls of few tiles): 4096 x 4096 takes
+// 17.2, 19.2 us (257, 384 rows) by pairs, 14.5, 16.8 by lone CTAs; 17408 x 5120 37.5, 38.5 (450, 512) against 41.2, 45.4.
 constexpr int kI8PairRows = 384;
 // Clusters of 0 .. 8 CTAs, one per SM, that start together on a B200.  Its occupancy calculator says 45, 26 and 22 of
 // 3, 5 and 6, but the last ones of these wait for others to end: 64 rows, K = 8080, 14.9, 17.4, 18.6, 23.0 us with 42

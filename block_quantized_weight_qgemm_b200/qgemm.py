@@ -416,6 +416,10 @@ def moe_gate_up(x: torch.Tensor, offsets: torch.Tensor, gate: ExpertTable, up: E
 # addresses, one pass of checks, sizes remembered per shape.  A call on another device than the
 # current one is made again with that device current (the library launches on the current device), one
 # with a stream of its own with that stream current, so that what it allocates belongs to that stream.
+#
+# Like every call of this binding they are unknown to autograd: results carry no graph, whether or not
+# the inputs require gradients.  A training step calls the gradients itself (from an autograd.Function of
+# its own, say); those of the experts' products between combine and dispatch are its own as well.
 
 _ROW_DTYPES = {torch.float32: Y_F32, torch.bfloat16: Y_BF16}
 
@@ -514,7 +518,8 @@ def _out(out, M, N, dtype, like):
 
 def moe_dispatch_grad(dxs: torch.Tensor, rows: torch.Tensor, dx: torch.Tensor | None = None,
                       dx_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-    """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x."""
+    """qgemm_moe_dispatch_grad: dx[t] = sum_j dxs[rows[t, j]], the gradient of moe_dispatch's x given that of
+    its xs (which the caller takes from the experts' backward)."""
     if stream is not None:
         return _on(stream, dxs, moe_dispatch_grad, dxs, rows, dx, dx_dtype)
     T, k, H = _routed(dxs, rows)
@@ -666,6 +671,7 @@ def i8_quant_x(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch
 
 @functools.lru_cache(maxsize=256)
 def i8_workspace_size(N: int, K: int, M: int) -> int:
+    """Bytes of workspace that is enough for every i8_run of at most M rows."""
     b = _SZ()
     _check(lib().qgemm_i8_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_workspace_size")
     return b.value
@@ -714,6 +720,7 @@ class I8ExpertTable:
 
 @functools.lru_cache(maxsize=256)
 def i8_moe_workspace_size(N: int, K: int, M: int) -> int:
+    """Bytes of workspace that is enough for every routed call of at most M rows."""
     b = _SZ()
     _check(lib().qgemm_i8_moe_workspace_size(N, K, M, ctypes.byref(b)), "qgemm_i8_moe_workspace_size")
     return b.value

@@ -54,6 +54,9 @@
  *     the operand's address and geometry; they hold no device memory).
  *   - qgemm_run, qgemm_ffn_gate_up and qgemm_i8_* calls that may overlap on the device need
  *     their own workspaces; qgemm_run_noalloc calls share one scratch and must not overlap.
+ *   - A workspace size is that of the width it is asked for, and a narrower call may need more
+ *     (K is split at decode widths): a workspace for several widths takes the largest of their
+ *     sizes.  The qgemm_i8_* sizes cover every narrower call by themselves.
  *   - The GEMM kernels are programmatic dependents of the small x-preparation kernel
  *     launched just before them and start streaming weights before they wait for it.  x
  *     (and every buffer a call writes) is ordered after all earlier work on the stream; the
@@ -357,6 +360,8 @@ int qgemm_bs_ffn_gate_up(int fmt, const void* x_dev, int64_t M, int64_t K, const
  * ys, dys, dxs hold T k rows; a value of rows_dev outside [0, T k) counts as -1, and no two slots
  * may name one row in qgemm_moe_combine_grad.  A slot without a row is not read: what its weight
  * or a row behind the last expert holds, NaN included, reaches no output.
+ * The gradients are those of the two row movers.  What lies between them, the experts' products,
+ * has none in this library: the way from dys back to dxs is the caller's.
  * Errors: QGEMM_ERR_FORMAT (types), _SHAPE, _NULL, _ALIGN, _DEVICE, _CUDA.
  */
 #define QGEMM_MOE_MAX_EXPERTS 4096
@@ -388,7 +393,8 @@ int qgemm_moe_combine_grad(const void* dy_dev, int dy_dtype, const void* ys_dev,
  * K: a multiple of 16 (QGEMM_ERR_K_BLOCK) and at most 131072 (QGEMM_ERR_SHAPE), which keeps the
  * sum inside int32 for codes of -128 .. 127.
  * Packed weights: codes in the tile-major layout of one-byte codes above (CK = 128), scales
- * float [N].  qgemm_i8_pack quantises fp32 W the same way per channel; qgemm_i8_repack_rowmajor
+ * float [N].  qgemm_i8_pack quantises fp32 W the same way per channel (codes clamped to +-127,
+ * which a channel of subnormals may need); qgemm_i8_repack_rowmajor
  * brings int8 codes [N][code_pitch] of a checkpoint into the layout (its scales are used as
  * they are).  qgemm_i8_quant_x is the row quantisation alone: codes int8 [M][K], scales [M].
  * Workspaces hold the codes and scales of x and, where K is split, int32 partials; a small call
