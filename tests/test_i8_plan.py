@@ -32,7 +32,7 @@ def plan(tmp_path_factory):
     assert cxx, "the tests build a host program with g++"
     d = tmp_path_factory.mktemp("plan")
     (d / "plan.cpp").write_text(PROGRAM)
-    cuda = os.path.dirname(os.path.dirname(qbuild.NVCC))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(qbuild.NVCC) or qbuild.NVCC)))
     subprocess.run([cxx, "-std=c++17", "-I", qbuild.CSRC, "-I", os.path.join(cuda, "include"), str(d / "plan.cpp"), lib,
                     "-L", os.path.join(cuda, "lib64"), "-lcudart", "-Wl,-rpath,%s:%s" % (os.path.dirname(lib), os.path.join(cuda, "lib64")),
                     "-o", str(d / "plan")], check=True, capture_output=True, text=True)
